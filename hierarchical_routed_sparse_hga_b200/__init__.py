@@ -21,12 +21,15 @@ from ._lib import (EXPORTS, HGA_BF16, HGA_ERR_CUDA, HGA_ERR_DEVICE_CHECK,  # noq
                    hga_route_workspace_size, hga_status_string,
                    hga_timing_collect, hga_timing_enable, hga_timing_get, hga_timing_kinds,
                    hga_timing_reset,
-                   hga_version, load, timing_table)
+                   hga_version, load, timing_table,
+                   PagedCache, hga_paged_append, hga_paged_decode,
+                   hga_paged_decode_workspace_size, hga_paged_evict,
+                   hga_paged_evict_workspace_size)
 
 
 def __getattr__(name):
     # HgaLayer needs torch; import it lazily so CPU-only tools stay light
-    if name in ("HgaLayer", "HgaTieredLayer", "HgaFileTieredLayer"):
+    if name in ("HgaLayer", "HgaTieredLayer", "HgaFileTieredLayer", "HgaPagedLayer"):
         from . import runtime
         return getattr(runtime, name)
     raise AttributeError(name)

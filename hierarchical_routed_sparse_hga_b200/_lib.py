@@ -33,9 +33,11 @@ EXPORTS = ("hga_version", "hga_status_string", "hga_last_cuda_error", "hga_build
            "hga_tier_stage_rows", "hga_tier_workspace_size", "hga_tier_gather",
            "hga_tier_append", "hga_decode", "hga_build_query_summaries",
            "hga_route_causal", "hga_prepare_segment", "hga_route_summarized",
-           "hga_tier_plan", "hga_tier_read_groups", "hga_tier_write_segment")
+           "hga_tier_plan", "hga_tier_read_groups", "hga_tier_write_segment",
+           "hga_paged_append", "hga_paged_decode_workspace_size", "hga_paged_decode",
+           "hga_paged_evict_workspace_size", "hga_paged_evict")
 HGA_NOALLOC_SCRATCH_BYTES = 4 << 20
-HGA_K_COUNT = 16
+HGA_K_COUNT = 20
 
 
 class HgaError(RuntimeError):
@@ -69,6 +71,76 @@ class Config:
         scale = self.scale if self.scale is not None else 1.0 / math.sqrt(self.head_dim)
         return _Config(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim,
                        self.topk_blocks, self.topk_groups, self.dtype, self.flags, scale)
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("slot_pos", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class PagedCache:
+    """Mirror of hga_pages_t over torch tensors (which it keeps alive).
+
+    k, v [n_pages, n_kv_heads, page_size, head_dim] of the config's type; each
+    page contiguous, any (common) stride from page to page, so the two may be
+    views of one [n_pages, 2, ...] tensor.  table [batch, max_pages] int32;
+    weight (float32) and slot_pos (int32), both [n_pages, n_kv_heads,
+    page_size], optional.  All on one CUDA device.
+    """
+
+    def __init__(self, cfg: Config, k, v, table, weight=None, slot_pos=None):
+        import torch
+        dt = torch.bfloat16 if cfg.dtype == HGA_BF16 else torch.float32
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim]")
+        n_pages, heads, page_size, d = k.shape
+        if (heads, d) != (cfg.n_kv_heads, cfg.head_dim):
+            raise ValueError(f"k has {heads} heads of {d}, the config {cfg.n_kv_heads} of "
+                             f"{cfg.head_dim}")
+        inner = (page_size * d, d, 1)
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != dt or t.shape != k.shape:
+                raise ValueError(f"{name} must be {dt} of shape {tuple(k.shape)}")
+            if any(n > 1 and s != w for n, s, w in zip(t.shape[1:], t.stride()[1:], inner)):
+                raise ValueError(f"each page of {name} must be contiguous")
+        if n_pages > 1 and k.stride(0) != v.stride(0):
+            raise ValueError("k and v must have the same page stride")
+        if table.dim() != 2 or table.shape[0] != cfg.batch or table.dtype != torch.int32:
+            raise ValueError(f"table must be int32 [{cfg.batch}, max_pages]")
+        records = (n_pages, heads, page_size)
+        for name, t, want in (("weight", weight, torch.float32),
+                              ("slot_pos", slot_pos, torch.int32)):
+            if t is not None and (t.dtype != want or tuple(t.shape) != records):
+                raise ValueError(f"{name} must be {want} of shape {records}")
+        for name, t in (("table", table), ("weight", weight), ("slot_pos", slot_pos)):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        for t in (k, v, table, weight, slot_pos):
+            if t is not None and (not t.is_cuda or t.device != k.device):
+                raise ValueError("a paged cache takes tensors of one CUDA device")
+        self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
+        self.device = k.device
+        self.n_pages, self.page_size, self.max_pages = n_pages, page_size, table.shape[1]
+        self.batch = cfg.batch
+        stride = k.stride(0) if n_pages > 1 else heads * page_size * d
+        self._c = _Pages(k.data_ptr(), v.data_ptr(), weight.data_ptr() if weight is not None else None,
+                         slot_pos.data_ptr() if slot_pos is not None else None, table.data_ptr(),
+                         n_pages, stride, page_size, self.max_pages)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def raw(cls, k, v, table, n_pages, page_stride, page_size, max_pages, weight=None,
+            slot_pos=None):
+        """The same over raw device addresses of the current device."""
+        self = cls.__new__(cls)
+        self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
+        self.device = self.batch = None
+        self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
+        self._c = _Pages(k, v, weight, slot_pos, table, n_pages, page_stride, page_size, max_pages)
+        self._ref = ctypes.byref(self._c)
+        return self
 
 
 _lib = None
@@ -130,6 +202,12 @@ def load() -> ctypes.CDLL:
                                                 P, P, I64, I32]),
         "hga_tier_write_segment": (ctypes.c_int, [CFG, ctypes.c_int, ctypes.c_int, I64, I64,
                                                   I32, P, P, I64, I32]),
+        "hga_paged_append": (ctypes.c_int, [CFG, P, P, P, P, I64, I64, I32, P, P, P,
+                                            ctypes.c_float, P, P]),
+        "hga_paged_decode_workspace_size": (SZ, [CFG, P, I32]),
+        "hga_paged_decode": (ctypes.c_int, [CFG, P, P, P, I32, P, P, P, SZ, P]),
+        "hga_paged_evict_workspace_size": (SZ, [CFG, P]),
+        "hga_paged_evict": (ctypes.c_int, [CFG, P, P, P, I32, I32, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -399,6 +477,104 @@ def hga_segment_fwd_bwd(cfg: Config, q, k, v, ctx_cap, q_begin, s_len, bsum, gsu
         ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), ctx_cap, q_begin, s_len, _ptr(bsum),
         _ptr(gsum), _ptr(sel_blk), _ptr(sel_grp), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq),
         _ptr(dk), _ptr(dv), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# paged key-value cache
+# ----------------------------------------------------------------------------
+
+def _paged_arg(cache: PagedCache, name, x, dtype, numel):
+    """Device address of a call's tensor (or raw address), checked against the
+    cache's device and the type and size the call reads or writes."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise ValueError("libhga takes device tensors")
+    if cache.device is not None and x.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device {cache.device}")
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not x.is_contiguous():
+        raise ValueError("libhga takes contiguous tensors")
+    if x.numel() < numel:
+        raise ValueError(f"{name} must hold {numel} elements")
+    return x.data_ptr()
+
+
+def _paged_dtype(cfg):
+    import torch
+    return torch.bfloat16 if cfg.dtype == HGA_BF16 else torch.float32
+
+
+def _paged_call(fn, cache: PagedCache, stream, *args):
+    """Calls fn on the cache's device, on `stream` or that device's current one."""
+    import torch
+    if cache.batch is not None and cache.batch != args[0]._obj.batch:
+        raise ValueError("the cache was described for another batch")
+    lib = load()
+    dev = cache.device
+    if dev is None or dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib, fn)(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib, fn)(*args, _stream(stream)))
+
+
+def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_row_stride,
+                     kv_row_stride, s_new, n_new, n_slots, pos, rope_base, q_out, stream=None):
+    """New tokens into the cache, from their projection outputs (contiguous
+    tensors, or raw addresses: three of one buffer for a fused QKV row)."""
+    import torch
+    dt, B = _paged_dtype(cfg), cfg.batch
+    rows, d = max(B * s_new, 1) - 1, cfg.head_dim
+    q_numel = rows * q_row_stride + cfg.n_q_heads * d
+    kv_numel = rows * kv_row_stride + cfg.n_kv_heads * d
+    _paged_call("hga_paged_append", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+                _paged_arg(cache, "q_proj", q_proj, dt, q_numel),
+                _paged_arg(cache, "k_proj", k_proj, dt, kv_numel),
+                _paged_arg(cache, "v_proj", v_proj, dt, kv_numel),
+                q_row_stride, kv_row_stride, s_new,
+                _paged_arg(cache, "n_new", n_new, torch.int32, B),
+                _paged_arg(cache, "n_slots", n_slots, torch.int32, B),
+                _paged_arg(cache, "pos", pos, torch.int64, B), float(rope_base or 0.0),
+                _paged_arg(cache, "q_out", q_out, dt, B * cfg.n_q_heads * s_new * cfg.head_dim))
+
+
+def hga_paged_decode_workspace_size(cfg: Config, cache: PagedCache, accumulate=False) -> int:
+    return int(load().hga_paged_decode_workspace_size(ctypes.byref(cfg.c()), cache._ref,
+                                                      int(accumulate)))
+
+
+def hga_paged_decode(cfg: Config, cache: PagedCache, q, n_slots, accumulate, o, lse, workspace,
+                     ws_bytes=None, stream=None):
+    """One new token per sequence over all its slots; accumulate adds every
+    slot's attention weight to cache.weight."""
+    import torch
+    dt, rows = _paged_dtype(cfg), cfg.batch * cfg.n_q_heads
+    ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    _paged_call("hga_paged_decode", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+                _paged_arg(cache, "q", q, dt, rows * cfg.head_dim),
+                _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch), int(accumulate),
+                _paged_arg(cache, "o", o, dt, rows * cfg.head_dim),
+                _paged_arg(cache, "lse", lse, torch.float32, rows),
+                _paged_arg(cache, "workspace", workspace, None, 0), ws_bytes)
+
+
+def hga_paged_evict_workspace_size(cfg: Config, cache: PagedCache) -> int:
+    return int(load().hga_paged_evict_workspace_size(ctypes.byref(cfg.c()), cache._ref))
+
+
+def hga_paged_evict(cfg: Config, cache: PagedCache, n_slots, pos, keep, sinks, recent, workspace,
+                    ws_bytes=None, stream=None):
+    """Cuts every sequence to `keep` slots per KV head by accumulated weight
+    (n_slots itself is the caller's to clamp)."""
+    import torch
+    ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    _paged_call("hga_paged_evict", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+                _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch),
+                _paged_arg(cache, "pos", pos, torch.int64, cfg.batch), keep, sinks, recent,
+                _paged_arg(cache, "workspace", workspace, None, 0), ws_bytes)
+
 
 def hga_get_device_status(stream=None) -> int:
     return int(load().hga_get_device_status(_stream(stream)))

@@ -23,6 +23,9 @@
 #include "tier.cuh"
 #include "decode.cuh"
 #include "prepare.cuh"
+#include "paged_append.cuh"
+#include "paged_decode.cuh"
+#include "paged_evict.cuh"
 #include "file_tier.h"
 #include "trace.cuh"
 
@@ -36,15 +39,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-hga_status_t check_cfg(const hga_config_t* c) {
+// routed: the call routes, so the top-k counts must be in range too
+hga_status_t check_cfg(const hga_config_t* c, bool routed = true) {
   if (!c) return HGA_ERR_INVALID_ARG;
   if (c->batch < 1 || c->n_kv_heads < 1 || c->n_q_heads < 1) return HGA_ERR_INVALID_ARG;
   if (c->n_q_heads % c->n_kv_heads != 0) return HGA_ERR_INVALID_ARG;
   if (c->n_q_heads / c->n_kv_heads > 8) return HGA_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128) return HGA_ERR_UNSUPPORTED;
   if (c->dtype != HGA_F32 && c->dtype != HGA_BF16) return HGA_ERR_UNSUPPORTED;
-  if (c->topk_blocks < 1 || c->topk_blocks > 64) return HGA_ERR_UNSUPPORTED;
-  if (c->topk_groups < 1 || c->topk_groups > 256) return HGA_ERR_UNSUPPORTED;
+  if (routed && (c->topk_blocks < 1 || c->topk_blocks > 64)) return HGA_ERR_UNSUPPORTED;
+  if (routed && (c->topk_groups < 1 || c->topk_groups > 256)) return HGA_ERR_UNSUPPORTED;
   if (!(c->scale > 0.f) || c->scale != c->scale) return HGA_ERR_INVALID_ARG;
   if (c->batch > 65535 || c->n_q_heads > 65535) return HGA_ERR_UNSUPPORTED;
   return HGA_OK;
@@ -829,7 +833,8 @@ const char* hga_kernel_name(int kind) {
       "summaries",      "route_qbar",        "route_block_topk",    "route_select",
       "attn_fwd_simt",  "attn_bwd_dq_simt",  "attn_bwd_dkdv_simt",  "attn_fwd_tc",
       "attn_bwd_dq_tc", "attn_bwd_dkdv_tc",  "tier_dedup",          "tier_copy",
-      "route_fused",    "decode",            "query_summaries",     "prepare"};
+      "route_fused",    "decode",            "query_summaries",     "prepare",
+      "paged_append",   "paged_decode",      "paged_join",          "paged_evict"};
   return (kind >= 0 && kind < HGA_K_COUNT) ? names[kind] : "unknown";
 }
 
@@ -1145,4 +1150,149 @@ extern "C" hga_status_t hga_tier_write_segment(const hga_config_t* cfg, int fd_k
                                    n_threads)
              ? HGA_OK
              : HGA_ERR_IO;
+}
+
+// ---------------------------------------------------------------------------
+// Paged key-value cache
+// ---------------------------------------------------------------------------
+namespace {
+
+hga_status_t check_pages(const hga_config_t* cfg, const hga_pages_t* c) {
+  hga_status_t st = check_cfg(cfg, false);
+  if (st != HGA_OK) return st;
+  if (!c || !c->k || !c->v || !c->table) return HGA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(c->k), static_cast<const void*>(c->v),
+                        static_cast<const void*>(c->weight),
+                        static_cast<const void*>(c->slot_pos),
+                        static_cast<const void*>(c->table)})
+    if (!aligned16(p)) return HGA_ERR_INVALID_ARG;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 &&
+      c->page_size != 256)
+    return HGA_ERR_UNSUPPORTED;
+  if (c->n_pages < 1 || c->max_pages < 1) return HGA_ERR_INVALID_ARG;
+  if (c->n_pages > 0x7fffffff || int64_t(c->max_pages) * c->page_size > (int64_t(1) << 30))
+    return HGA_ERR_UNSUPPORTED;
+  const int64_t elt = cfg->dtype == HGA_BF16 ? 2 : 4;
+  if (c->page_stride < int64_t(cfg->n_kv_heads) * c->page_size * cfg->head_dim ||
+      c->page_stride > (int64_t(1) << 40) || c->page_stride * elt % 16 != 0)
+    return HGA_ERR_INVALID_ARG;
+  return HGA_OK;
+}
+
+PagedView paged_view(const hga_config_t* cfg, const hga_pages_t* c) {
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  return {c->k,        c->v,           c->weight, c->slot_pos,  c->table,
+          c->n_pages,  c->page_stride, shift,     c->max_pages, cfg->n_kv_heads};
+}
+
+}  // namespace
+
+extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_pages_t* cache,
+                                         const void* q_proj, const void* k_proj,
+                                         const void* v_proj, int64_t q_row_stride,
+                                         int64_t kv_row_stride, int32_t s_new,
+                                         const int32_t* n_new, const int32_t* n_slots,
+                                         const int64_t* pos, float rope_base, void* q_out,
+                                         void* stream) {
+  hga_status_t st = check_pages(cfg, cache);
+  if (st != HGA_OK) return st;
+  if (!k_proj || !v_proj || !n_slots || !pos || (q_proj == nullptr) != (q_out == nullptr))
+    return HGA_ERR_INVALID_ARG;
+  for (const void* p : {q_proj, k_proj, v_proj, static_cast<const void*>(n_new),
+                        static_cast<const void*>(n_slots), static_cast<const void*>(pos),
+                        static_cast<const void*>(q_out)})
+    if (!aligned16(p)) return HGA_ERR_INVALID_ARG;
+  if (s_new < 0 || !(rope_base >= 0.f)) return HGA_ERR_INVALID_ARG;
+  const int64_t elt = cfg->dtype == HGA_BF16 ? 2 : 4;
+  const int64_t max_stride = int64_t(1) << 32;
+  if (kv_row_stride < int64_t(cfg->n_kv_heads) * cfg->head_dim || kv_row_stride * elt % 16 != 0 ||
+      kv_row_stride > max_stride)
+    return HGA_ERR_INVALID_ARG;
+  if (q_proj && (q_row_stride < int64_t(cfg->n_q_heads) * cfg->head_dim ||
+                 q_row_stride * elt % 16 != 0 || q_row_stride > max_stride))
+    return HGA_ERR_INVALID_ARG;
+  if (s_new == 0) return HGA_OK;
+  const PagedView view = paged_view(cfg, cache);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const double log2_base = rope_base > 1.f ? std::log2(double(rope_base)) : 0.0;
+  return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
+    dim3 grid(s_new, cfg->batch);
+    return traced_launch(HGA_K_PAGED_APPEND, s, [&] {
+      return launch_pdl(paged_append_kernel<T, D>, grid, dim3(kAppendThreads), 0, s, view,
+          static_cast<const T*>(q_proj), static_cast<const T*>(k_proj),
+          static_cast<const T*>(v_proj), q_row_stride, kv_row_stride, s_new, n_new, n_slots, pos,
+          cfg->n_q_heads, log2_base, static_cast<T*>(q_out));
+    });
+  });
+}
+
+extern "C" size_t hga_paged_decode_workspace_size(const hga_config_t* cfg,
+                                                  const hga_pages_t* cache, int32_t accumulate) {
+  if (check_pages(cfg, cache) != HGA_OK) return 0;
+  return 256;
+}
+
+extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_pages_t* cache,
+                                         const void* q, const int32_t* n_slots,
+                                         int32_t accumulate, void* o, float* lse, void* workspace,
+                                         size_t ws_bytes, void* stream) {
+  hga_status_t st = check_pages(cfg, cache);
+  if (st != HGA_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return HGA_ERR_INVALID_ARG;
+  if (accumulate && !cache->weight) return HGA_ERR_INVALID_ARG;
+  for (const void* p : {q, static_cast<const void*>(n_slots), static_cast<const void*>(o),
+                        static_cast<const void*>(lse), static_cast<const void*>(workspace)})
+    if (!p || !aligned16(p)) return HGA_ERR_INVALID_ARG;
+  if (ws_bytes < hga_paged_decode_workspace_size(cfg, cache, accumulate))
+    return HGA_ERR_WORKSPACE;
+  const PagedView view = paged_view(cfg, cache);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const float scale_log2 = cfg->scale * 1.4426950408889634f;
+  return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
+    dim3 grid(cfg->n_kv_heads, cfg->batch);
+    return traced_launch(HGA_K_PAGED_DECODE, s, [&] {
+      return launch_pdl(pdec::paged_decode_kernel<T, D>, grid, dim3(pdec::kThreads), 0, s, view,
+          static_cast<const T*>(q), n_slots, cfg->n_q_heads / cfg->n_kv_heads, accumulate,
+          scale_log2, static_cast<T*>(o), lse);
+    });
+  });
+}
+
+extern "C" size_t hga_paged_evict_workspace_size(const hga_config_t* cfg,
+                                                 const hga_pages_t* cache) {
+  if (check_pages(cfg, cache) != HGA_OK) return 0;
+  const size_t slots =
+      size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size;
+  return align256(slots * 4) + align256(slots) + align256(slots * 4);
+}
+
+extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
+                                        const int32_t* n_slots, const int64_t* pos, int32_t keep,
+                                        int32_t sinks, int32_t recent, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  hga_status_t st = check_pages(cfg, cache);
+  if (st != HGA_OK) return st;
+  if (!cache->weight || !cache->slot_pos) return HGA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(n_slots), static_cast<const void*>(pos),
+                        static_cast<const void*>(workspace)})
+    if (!p || !aligned16(p)) return HGA_ERR_INVALID_ARG;
+  if (keep < 1 || sinks < 0 || recent < 0 || int64_t(sinks) + recent > keep)
+    return HGA_ERR_INVALID_ARG;
+  if (ws_bytes < hga_paged_evict_workspace_size(cfg, cache)) return HGA_ERR_WORKSPACE;
+  const PagedView view = paged_view(cfg, cache);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t slots =
+      size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size;
+  char* ws = static_cast<char*>(workspace);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ws);
+  int32_t* moves = reinterpret_cast<int32_t*>(ws + align256(slots * 4));
+  uint8_t* flags = reinterpret_cast<uint8_t*>(ws + 2 * align256(slots * 4));
+  return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
+    dim3 grid(cfg->n_kv_heads, cfg->batch);
+    return traced_launch(HGA_K_PAGED_EVICT, s, [&] {
+      return launch_pdl(pev::paged_evict_kernel<T, D>, grid, dim3(pev::kThreads), 0, s, view,
+          n_slots, pos, keep, sinks, recent, keys, flags, moves);
+    });
+  });
 }

@@ -323,3 +323,107 @@ class HgaFileTieredLayer(HgaTieredLayer):
         _lib.hga_tier_write_segment(self.cfg, self.fd_k, self.fd_v, self.ctx_cap, q_begin,
                                     self.seg_len, self.k_seg_host, self.v_seg_host,
                                     self.seg_len, self.n_threads)
+
+
+class HgaPagedLayer:
+    """One layer's paged key-value cache for serving: exact attention of one
+    new token per sequence over every cached token, and eviction by the
+    accumulated attention weight.
+
+    The pool (k, v [n_pages, n_kv_heads, page_size, head_dim]), the page table
+    [batch, max_pages] and the per-slot records are allocated here unless
+    given; with n_pages >= batch * max_pages every sequence starts with
+    max_pages pages of its own, otherwise the caller fills `table`.  n_slots
+    (int32 [batch], slots in use) and pos (int64 [batch], position of the last
+    token, -1 before the first) live on the device and may be shared by the
+    layers of a model.  A step is
+
+        advance(n_new); append(...); decode(...)      [; evict(keep, ...)]
+
+    with one `advance` per step however many layers share the counts.
+    """
+
+    def __init__(self, cfg: Config, n_pages: int, page_size: int, max_pages: int, device="cuda",
+                 k=None, v=None, table=None, n_slots=None, pos=None, records=True):
+        self.cfg, self.page_size, self.max_pages = cfg, page_size, max_pages
+        dev = torch.device(device)
+        dt = _TORCH_DTYPE[cfg.dtype]
+        B = cfg.batch
+        shape = (n_pages, cfg.n_kv_heads, page_size, cfg.head_dim)
+        self.k = k if k is not None else torch.zeros(shape, dtype=dt, device=dev)
+        self.v = v if v is not None else torch.zeros(shape, dtype=dt, device=dev)
+        if table is None:
+            table = torch.full((B, max_pages), -1, dtype=torch.int32, device=dev)
+            if n_pages >= B * max_pages:
+                table.view(-1).copy_(torch.arange(B * max_pages, dtype=torch.int32, device=dev))
+        self.table = table
+        self.weight = torch.zeros(shape[:3], dtype=torch.float32, device=dev) if records else None
+        self.slot_pos = torch.full(shape[:3], -1, dtype=torch.int32,
+                                   device=dev) if records else None
+        self.n_slots = n_slots if n_slots is not None else torch.zeros(B, dtype=torch.int32,
+                                                                       device=dev)
+        self.pos = pos if pos is not None else torch.full((B,), -1, dtype=torch.int64, device=dev)
+        self.cache = _lib.PagedCache(cfg, self.k, self.v, self.table, self.weight, self.slot_pos)
+        ws = _lib.hga_paged_decode_workspace_size(cfg, self.cache, records)
+        if records:
+            ws = max(ws, _lib.hga_paged_evict_workspace_size(cfg, self.cache))
+        self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+
+    def advance(self, n_new):
+        """n_new (an int, or an int32 tensor [batch]) tokens join each sequence."""
+        self.n_slots.add_(n_new)
+        self.pos.add_(n_new)
+
+    @staticmethod
+    def _rows(x, heads, d, name):
+        """Row stride of token-major projections [batch, s_new, heads, d] (or
+        [batch, s_new, heads*d]), which may be a column range of a fused row."""
+        B, S = x.shape[:2]
+        inner = (d, 1) if x.dim() == 4 else (1,)
+        if x.dim() not in (3, 4) or x[0, 0].numel() != heads * d:
+            raise ValueError(f"{name} must be [batch, s_new, {heads}, {d}]")
+        if any(n > 1 and s != w for n, s, w in zip(x.shape[2:], x.stride()[2:], inner)):
+            raise ValueError(f"the rows of {name} must be contiguous")
+        row = x.stride(1) if S > 1 else x.stride(0) if B > 1 else heads * d
+        if B > 1 and x.stride(0) != S * row:
+            raise ValueError(f"the tokens of {name} must lie one row stride apart")
+        return row
+
+    def append(self, q_proj, k_proj, v_proj, rope_base, q_out, n_new=None, stream=None):
+        """The new tokens' projections (token-major, possibly column ranges of
+        one fused QKV tensor) into the slots that `advance` counted; Q rotated
+        into q_out [batch, n_q_heads, s_new, d].  n_new (int32 [batch]): how
+        many rows of each sequence are tokens (all, if None)."""
+        cfg, d = self.cfg, self.cfg.head_dim
+        for name, x in (("q_proj", q_proj), ("k_proj", k_proj), ("v_proj", v_proj)):
+            if x is not None and (x.device != self.cache.device
+                                  or x.dtype != _TORCH_DTYPE[cfg.dtype]
+                                  or x.shape[:2] != k_proj.shape[:2] or x.shape[0] != cfg.batch):
+                raise ValueError(f"{name}: type, device, batch or token count differ")
+        kv_row = self._rows(k_proj, cfg.n_kv_heads, d, "k_proj")
+        if self._rows(v_proj, cfg.n_kv_heads, d, "v_proj") != kv_row:
+            raise ValueError("k_proj and v_proj must have the same row stride")
+        q_row = 0 if q_proj is None else self._rows(q_proj, cfg.n_q_heads, d, "q_proj")
+        _lib.hga_paged_append(cfg, self.cache, None if q_proj is None else q_proj.data_ptr(),
+                              k_proj.data_ptr(), v_proj.data_ptr(), q_row, kv_row,
+                              k_proj.shape[1], n_new, self.n_slots, self.pos, rope_base, q_out,
+                              stream)
+
+    def decode(self, q, o, lse, accumulate=False, stream=None):
+        """One new token per sequence: q, o [batch, n_q_heads, d], lse
+        [batch, n_q_heads]; accumulate adds to the slots' weights."""
+        _lib.hga_paged_decode(self.cfg, self.cache, q, self.n_slots, accumulate, o, lse,
+                              self.workspace, stream=stream)
+
+    def evict(self, keep: int, sinks: int = 0, recent: int = 0, stream=None, clamp=True):
+        """Cuts every sequence to `keep` slots.  clamp=False leaves n_slots as
+        it is, for layers that share it: pass True with the last of them."""
+        _lib.hga_paged_evict(self.cfg, self.cache, self.n_slots, self.pos, keep, sinks, recent,
+                             self.workspace, stream=stream)
+        if clamp:
+            if stream is None:
+                stream = torch.cuda.current_stream(self.cache.device)
+            elif isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.cache.device)
+            with torch.cuda.stream(stream):
+                self.n_slots.clamp_(max=keep)

@@ -475,6 +475,124 @@ HGA_API hga_status_t hga_tier_write_segment(const hga_config_t* cfg, int fd_k, i
                                             int64_t seg_rows, int32_t n_threads);
 
 /*
+ * Paged key-value cache -- for serving sequences of any length from one pool
+ * (the pages name generation as a use [A] and leave the cache open; these
+ * calls attend to every cached token, without routing).
+ *
+ * The pool holds n_pages pages of page_size slots.  Slot r of KV head h of
+ * page p is row [h, r] of the page: its key is the head_dim elements at
+ * k + p*page_stride + (h*page_size + r)*head_dim, its value the same in v
+ * (page_stride elements from one page to the next, at least
+ * n_kv_heads*page_size*head_dim, a multiple of 16 bytes; K and V may lie side
+ * by side in one allocation).  Slot s of sequence b is row s % page_size of
+ * page table[b*max_pages + s/page_size].  weight and slot_pos are records
+ * [n_pages, n_kv_heads, page_size] of every slot: the attention weight
+ * accumulated by hga_paged_decode and the position of the slot's token; each
+ * may be NULL where a call does not need it.
+ *
+ * n_slots [batch] (int32) counts the slots in use of each sequence, the new
+ * tokens of this step included, and pos [batch] (int64) is the position of
+ * its last token: a step advances both, then calls hga_paged_append and
+ * hga_paged_decode of every layer.  A sequence with n_slots = 0 is idle.
+ *
+ * Two sequences may share pages that they only read or decode from.  Pages
+ * that hga_paged_append writes or hga_paged_evict cuts belong to one sequence
+ * of the call.
+ *
+ * cfg->topk_blocks and cfg->topk_groups are not used by these calls.  Device
+ * checks: a count outside [0, max_pages*page_size] leaves the sequence's
+ * outputs and pages untouched, and a page outside [0, n_pages) is not
+ * accessed (what that means for each call stands below); both latch
+ * HGA_ERR_DEVICE_CHECK.
+ */
+typedef struct {
+  void* k;                /* pool of keys (cfg->dtype) */
+  void* v;                /* pool of values */
+  float* weight;          /* [n_pages, n_kv_heads, page_size], or NULL */
+  int32_t* slot_pos;      /* [n_pages, n_kv_heads, page_size], or NULL */
+  const int32_t* table;   /* [batch, max_pages] */
+  int64_t n_pages;        /* 1 .. 2^31 - 1 */
+  int64_t page_stride;    /* elements */
+  int32_t page_size;      /* 16, 32, 64, 128 or 256 */
+  int32_t max_pages;      /* columns of the table; max_pages*page_size <= 2^30 */
+} hga_pages_t;
+
+/*
+ * New tokens into the cache, from their projection outputs.  q_proj
+ * [batch, s_new, n_q_heads, head_dim], k_proj and v_proj [batch, s_new,
+ * n_kv_heads, head_dim], token-major, with the row strides of
+ * hga_prepare_segment (elements; batch b starts s_new rows after batch b-1).
+ * The first n_new[b] of sequence b's s_new rows are its new tokens (n_new
+ * NULL: all of them; 0 <= n_new[b] <= n_slots[b]); row i goes to slot
+ * n_slots[b] - n_new[b] + i and has position pos[b] - n_new[b] + 1 + i, which
+ * must lie in [0, 2^31).  Q and K are rotated as in hga_prepare_segment
+ * (rope_base 0 or 1: not rotated), V is not.  q_out [batch, n_q_heads, s_new,
+ * head_dim] receives Q; q_proj and q_out may both be NULL (K and V only).
+ * Where the records are kept, a new slot's weight becomes 0 and its slot_pos
+ * its position.  Rows i >= n_new[b] of q_out are left as they were.  A
+ * sequence whose counts or positions are out of range is left out, and a
+ * token whose page is out of range is not stored (its Q is); both latch
+ * HGA_ERR_DEVICE_CHECK.  One launch; no workspace.
+ */
+HGA_API hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_pages_t* cache,
+                                      const void* q_proj, const void* k_proj,
+                                      const void* v_proj, int64_t q_row_stride,
+                                      int64_t kv_row_stride, int32_t s_new,
+                                      const int32_t* n_new, const int32_t* n_slots,
+                                      const int64_t* pos, float rope_base, void* q_out,
+                                      void* stream);
+
+/* Bytes of device workspace hga_paged_decode needs (0 for bad arguments). */
+HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hga_pages_t* cache,
+                                               int32_t accumulate);
+
+/*
+ * Attention of one new token per sequence over all its n_slots[b] slots:
+ *   s_j = scale q.k_j;  O = softmax(s) V;  LSE = log(sum_j exp(s_j))
+ * for each of the G heads of every KV head.  q, o [batch, n_q_heads,
+ * head_dim] (cfg->dtype), lse [batch, n_q_heads] float32.  accumulate = 1
+ * adds the softmax weight of every slot, summed over the G heads, to
+ * cache->weight (which must then not be NULL):
+ *   weight[slot] += sum_g exp(s_gj - LSE_g).
+ * n_slots[b] = 0: O = 0, LSE = -inf.  Slots on a page outside [0, n_pages)
+ * are left out of the softmax.  Rows of the last page behind n_slots[b] are
+ * never used, whatever they hold.  Deterministic (with accumulate = 1 as long
+ * as no two sequences share a page).  workspace: at least
+ * hga_paged_decode_workspace_size() bytes of device memory, 16-byte aligned,
+ * whose contents do not matter; not used by two calls at once.
+ */
+HGA_API hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_pages_t* cache,
+                                      const void* q, const int32_t* n_slots, int32_t accumulate,
+                                      void* o, float* lse, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* Bytes of device workspace hga_paged_evict needs (0 for bad arguments). */
+HGA_API size_t hga_paged_evict_workspace_size(const hga_config_t* cfg, const hga_pages_t* cache);
+
+/*
+ * Cuts every sequence with more than `keep` slots to `keep`, per KV head, by
+ * accumulated weight.  Kept are the slots whose token's position is below
+ * `sinks` or above pos[b] - recent, then those with the largest weight, until
+ * `keep` are kept (ties, and slots beyond `keep` that would all have to be
+ * kept: the lower slot; a NaN weight counts as the smallest).  Attention does
+ * not depend on the order of the slots, so only what has to move moves: the
+ * kept slots at or behind `keep`, in ascending order, are copied with their
+ * records into the dropped slots before it, in ascending order.  Afterwards
+ * the kept tokens fill slots [0, keep); slots behind are left as they were.
+ * The caller then sets n_slots[b] to min(n_slots[b], keep) (the call does not,
+ * since the layers of a model share the counts) and may free the pages behind.
+ * Needs cache->weight and cache->slot_pos.  keep >= 1, sinks and recent >= 0,
+ * sinks + recent <= keep.  A sequence with more than `keep` slots that has a
+ * page out of range among them is left untouched (HGA_ERR_DEVICE_CHECK is
+ * latched).  workspace as above: at least hga_paged_evict_workspace_size()
+ * bytes.
+ */
+HGA_API hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
+                                     const int32_t* n_slots, const int64_t* pos, int32_t keep,
+                                     int32_t sinks, int32_t recent, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/*
  * Reads and clears the calling device's latched device-side status
  * (HGA_OK, HGA_ERR_DEVICE_CHECK or HGA_ERR_TIMEOUT).  Synchronises `stream`.
  */
@@ -514,7 +632,11 @@ typedef enum {
   HGA_K_DECODE = 13,
   HGA_K_QSUM = 14,
   HGA_K_PREPARE = 15,
-  HGA_K_COUNT = 16
+  HGA_K_PAGED_APPEND = 16,
+  HGA_K_PAGED_DECODE = 17,
+  HGA_K_PAGED_JOIN = 18,
+  HGA_K_PAGED_EVICT = 19,
+  HGA_K_COUNT = 20
 } hga_kernel_kind_t;
 
 /* Name of a kernel kind ("attn_fwd_simt", ...). */
