@@ -1186,6 +1186,35 @@ PagedView paged_view(const hga_config_t* cfg, const hga_pages_t* c) {
           c->n_pages,  c->page_stride, shift,     c->max_pages, cfg->n_kv_heads};
 }
 
+struct PagedWork {
+  pdec::Work work;
+  size_t bytes;
+};
+
+// The decode workspace: the units before each sequence, the partial results,
+// and (with weights) a score per slot and query head; 256-byte sections.
+PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumulate, void* base) {
+  const int d = cfg->head_dim, G = cfg->n_q_heads / cfg->n_kv_heads;
+  const size_t first_bytes = align256(size_t(cfg->batch + 1) * 8);
+  const size_t part_bytes = align256(size_t(2) * pdec::kBlocks * G * (d + 2) * 4);
+  const bool bf16 = cfg->dtype == HGA_BF16;
+  const int unit = bf16 ? (d == 128 ? pdec::Tile<__nv_bfloat16, 128>::kUnit
+                                    : pdec::Tile<__nv_bfloat16, 64>::kUnit)
+                        : (d == 128 ? pdec::Tile<float, 128>::kUnit : pdec::Tile<float, 64>::kUnit);
+  const size_t slots = (size_t(c->max_pages) * c->page_size + unit - 1) / unit * unit;
+  const size_t score_bytes =
+      accumulate ? align256(slots * cfg->batch * cfg->n_q_heads * 4) : 0;
+  char* p = static_cast<char*>(base);
+  PagedWork w = {};
+  w.bytes = first_bytes + part_bytes + score_bytes;
+  if (base) {
+    w.work.first = reinterpret_cast<int64_t*>(p);
+    w.work.part = reinterpret_cast<float*>(p + first_bytes);
+    if (accumulate) w.work.scores = reinterpret_cast<float*>(p + first_bytes + part_bytes);
+  }
+  return w;
+}
+
 }  // namespace
 
 extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_pages_t* cache,
@@ -1230,7 +1259,7 @@ extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_page
 extern "C" size_t hga_paged_decode_workspace_size(const hga_config_t* cfg,
                                                   const hga_pages_t* cache, int32_t accumulate) {
   if (check_pages(cfg, cache) != HGA_OK) return 0;
-  return 256;
+  return paged_work(cfg, cache, accumulate != 0, nullptr).bytes;
 }
 
 extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_pages_t* cache,
@@ -1250,11 +1279,19 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const float scale_log2 = cfg->scale * 1.4426950408889634f;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    dim3 grid(cfg->n_kv_heads, cfg->batch);
-    return traced_launch(HGA_K_PAGED_DECODE, s, [&] {
-      return launch_pdl(pdec::paged_decode_kernel<T, D>, grid, dim3(pdec::kThreads), 0, s, view,
-          static_cast<const T*>(q), n_slots, cfg->n_q_heads / cfg->n_kv_heads, accumulate,
-          scale_log2, static_cast<T*>(o), lse);
+    const int G = cfg->n_q_heads / cfg->n_kv_heads;
+    const pdec::Work work = paged_work(cfg, cache, accumulate != 0, workspace).work;
+    hga_status_t e = traced_launch(HGA_K_PAGED_DECODE, s, [&] {
+      return launch_pdl(pdec::paged_decode_kernel<T, D>, dim3(pdec::kBlocks), dim3(pdec::kThreads),
+          0, s, view, static_cast<const T*>(q), n_slots, cfg->batch, G, scale_log2,
+          static_cast<T*>(o), lse, work);
+    });
+    if (e != HGA_OK) return e;
+    const int joins = cfg->batch * cfg->n_q_heads;
+    dim3 grid(joins + (accumulate ? 4 * pdec::kBlocks : 0));
+    return traced_launch(HGA_K_PAGED_JOIN, s, [&] {
+      return launch_pdl(pdec::paged_join_kernel<T, D>, grid, dim3(pdec::kJoinThreads), 0, s, view,
+          n_slots, cfg->batch, G, joins, static_cast<T*>(o), lse, work);
     });
   });
 }
