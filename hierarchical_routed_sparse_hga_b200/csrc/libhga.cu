@@ -1299,9 +1299,9 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
 extern "C" size_t hga_paged_evict_workspace_size(const hga_config_t* cfg,
                                                  const hga_pages_t* cache) {
   if (check_pages(cfg, cache) != HGA_OK) return 0;
-  const size_t slots =
-      size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size;
-  return align256(slots * 4) + align256(slots) + align256(slots * 4);
+  // a (page, row) of every hole and mover: at most one entry per slot
+  return align256(size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size *
+                  sizeof(int2));
 }
 
 extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
@@ -1319,17 +1319,38 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   if (ws_bytes < hga_paged_evict_workspace_size(cfg, cache)) return HGA_ERR_WORKSPACE;
   const PagedView view = paged_view(cfg, cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t slots =
-      size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size;
-  char* ws = static_cast<char*>(workspace);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(ws);
-  int32_t* moves = reinterpret_cast<int32_t*>(ws + align256(slots * 4));
-  uint8_t* flags = reinterpret_cast<uint8_t*>(ws + 2 * align256(slots * 4));
+  // cluster size: enough blocks to fill the GPU about twice (four fit on an
+  // SM), but no share below 1024 slots of the table's width, where the
+  // cluster's barriers would cost more than the share
+  const int64_t heads = int64_t(cfg->batch) * cfg->n_kv_heads;
+  const int64_t slots = int64_t(cache->max_pages) * cache->page_size;
+  int nc = pev::kMaxC;
+  while (nc > 1 && (heads * nc > 2 * int64_t(sm_count()) || slots / nc < 1024)) nc /= 2;
+  const int key_cap = int(std::min<int64_t>(pev::kKeyCap, ((slots + nc - 1) / nc + 3) & ~int64_t(3)));
+  const size_t smem = size_t(key_cap) * 4;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    dim3 grid(cfg->n_kv_heads, cfg->batch);
+    // the limit counts the kernel's static shared memory too
+    hga_status_t e = ensure_smem(reinterpret_cast<const void*>(&pev::paged_evict_kernel<T, D>),
+                                 smem + sizeof(pev::Shared));
+    if (e != HGA_OK) return e;
     return traced_launch(HGA_K_PAGED_EVICT, s, [&] {
-      return launch_pdl(pev::paged_evict_kernel<T, D>, grid, dim3(pev::kThreads), 0, s, view,
-          n_slots, pos, keep, sinks, recent, keys, flags, moves);
+      cudaLaunchConfig_t lc = {};
+      lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
+      lc.blockDim = dim3(pev::kThreads);
+      lc.dynamicSmemBytes = smem;
+      lc.stream = s;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = unsigned(nc);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[1].val.programmaticStreamSerializationAllowed = 1;
+      lc.attrs = attr;
+      lc.numAttrs = 2;
+      return cudaLaunchKernelEx(&lc, pev::paged_evict_kernel<T, D>, view, n_slots, pos, int(keep),
+                                int(sinks), int(recent), key_cap,
+                                static_cast<int2*>(workspace));
     });
   });
 }
