@@ -121,7 +121,7 @@ class PagedCache:
             if t is not None and (not t.is_cuda or t.device != k.device):
                 raise ValueError("a paged cache takes tensors of one CUDA device")
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
-        self.device = k.device
+        self.device, self.index, self.dtype = k.device, k.get_device(), dt
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, table.shape[1]
         self.batch = cfg.batch
         stride = k.stride(0) if n_pages > 1 else heads * page_size * d
@@ -136,7 +136,7 @@ class PagedCache:
         """The same over raw device addresses of the current device."""
         self = cls.__new__(cls)
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
-        self.device = self.batch = None
+        self.device = self.index = self.dtype = self.batch = None
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self._c = _Pages(k, v, weight, slot_pos, table, n_pages, page_stride, page_size, max_pages)
         self._ref = ctypes.byref(self._c)
@@ -490,9 +490,9 @@ def _paged_arg(cache: PagedCache, name, x, dtype, numel):
         return x
     if not x.is_cuda:
         raise ValueError("libhga takes device tensors")
-    if cache.device is not None and x.device != cache.device:
+    if cache.index is not None and x.get_device() != cache.index:
         raise ValueError(f"{name} must be on the cache's device {cache.device}")
-    if dtype is not None and x.dtype != dtype:
+    if dtype is not None and x.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
     if not x.is_contiguous():
         raise ValueError("libhga takes contiguous tensors")
@@ -501,23 +501,20 @@ def _paged_arg(cache: PagedCache, name, x, dtype, numel):
     return x.data_ptr()
 
 
-def _paged_dtype(cfg):
-    import torch
-    return torch.bfloat16 if cfg.dtype == HGA_BF16 else torch.float32
-
-
-def _paged_call(fn, cache: PagedCache, stream, *args):
+def _paged_call(name, fn, cache: PagedCache, cfg: _Config, stream, *args):
     """Calls fn on the cache's device, on `stream` or that device's current one."""
-    import torch
-    if cache.batch is not None and cache.batch != args[0]._obj.batch:
+    if cache.batch is not None and cache.batch != cfg.batch:
         raise ValueError("the cache was described for another batch")
-    lib = load()
-    dev = cache.device
-    if dev is None or dev.index == torch.cuda.current_device():
-        _check(fn, getattr(lib, fn)(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn, getattr(lib, fn)(*args, _stream(stream)))
+    if cache.index is not None:
+        import torch
+        if cache.index != torch.cuda.current_device():
+            with torch.cuda.device(cache.index):
+                return _check(name, fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream)))
+        if stream is None:  # the address alone: a stream object costs 3 us
+            stream = torch._C._cuda_getCurrentRawStream(cache.index)
+    status = fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream))
+    if status != HGA_OK:
+        _check(name, status)
 
 
 def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_row_stride,
@@ -525,11 +522,11 @@ def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_r
     """New tokens into the cache, from their projection outputs (contiguous
     tensors, or raw addresses: three of one buffer for a fused QKV row)."""
     import torch
-    dt, B = _paged_dtype(cfg), cfg.batch
+    dt, B = cache.dtype, cfg.batch
     rows, d = max(B * s_new, 1) - 1, cfg.head_dim
     q_numel = rows * q_row_stride + cfg.n_q_heads * d
     kv_numel = rows * kv_row_stride + cfg.n_kv_heads * d
-    _paged_call("hga_paged_append", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+    _paged_call("hga_paged_append", load().hga_paged_append, cache, cfg.c(), stream,
                 _paged_arg(cache, "q_proj", q_proj, dt, q_numel),
                 _paged_arg(cache, "k_proj", k_proj, dt, kv_numel),
                 _paged_arg(cache, "v_proj", v_proj, dt, kv_numel),
@@ -550,9 +547,9 @@ def hga_paged_decode(cfg: Config, cache: PagedCache, q, n_slots, accumulate, o, 
     """One new token per sequence over all its slots; accumulate adds every
     slot's attention weight to cache.weight."""
     import torch
-    dt, rows = _paged_dtype(cfg), cfg.batch * cfg.n_q_heads
+    dt, rows = cache.dtype, cfg.batch * cfg.n_q_heads
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _paged_call("hga_paged_decode", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+    _paged_call("hga_paged_decode", load().hga_paged_decode, cache, cfg.c(), stream,
                 _paged_arg(cache, "q", q, dt, rows * cfg.head_dim),
                 _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch), int(accumulate),
                 _paged_arg(cache, "o", o, dt, rows * cfg.head_dim),
@@ -570,7 +567,7 @@ def hga_paged_evict(cfg: Config, cache: PagedCache, n_slots, pos, keep, sinks, r
     (n_slots itself is the caller's to clamp)."""
     import torch
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _paged_call("hga_paged_evict", cache, stream, ctypes.byref(cfg.c()), cache._ref,
+    _paged_call("hga_paged_evict", load().hga_paged_evict, cache, cfg.c(), stream,
                 _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch),
                 _paged_arg(cache, "pos", pos, torch.int64, cfg.batch), keep, sinks, recent,
                 _paged_arg(cache, "workspace", workspace, None, 0), ws_bytes)

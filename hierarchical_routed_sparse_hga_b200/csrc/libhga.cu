@@ -1191,11 +1191,11 @@ struct PagedWork {
   size_t bytes;
 };
 
-// The decode workspace: the units before each sequence, the partial results,
+// The decode workspace: the blocks' runs, the partial results,
 // and (with weights) a score per slot and query head; 256-byte sections.
 PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumulate, void* base) {
   const int d = cfg->head_dim, G = cfg->n_q_heads / cfg->n_kv_heads;
-  const size_t first_bytes = align256(size_t(cfg->batch + 1) * 8);
+  const size_t runs_bytes = align256(sizeof(pdec::Run) * pdec::kBlocks);
   const size_t part_bytes = align256(size_t(2) * pdec::kBlocks * G * (d + 2) * 4);
   const bool bf16 = cfg->dtype == HGA_BF16;
   const int unit = bf16 ? (d == 128 ? pdec::Tile<__nv_bfloat16, 128>::kUnit
@@ -1206,11 +1206,11 @@ PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumul
       accumulate ? align256(slots * cfg->batch * cfg->n_q_heads * 4) : 0;
   char* p = static_cast<char*>(base);
   PagedWork w = {};
-  w.bytes = first_bytes + part_bytes + score_bytes;
+  w.bytes = runs_bytes + part_bytes + score_bytes;
   if (base) {
-    w.work.first = reinterpret_cast<int64_t*>(p);
-    w.work.part = reinterpret_cast<float*>(p + first_bytes);
-    if (accumulate) w.work.scores = reinterpret_cast<float*>(p + first_bytes + part_bytes);
+    w.work.runs = reinterpret_cast<pdec::Run*>(p);
+    w.work.part = reinterpret_cast<float*>(p + runs_bytes);
+    if (accumulate) w.work.scores = reinterpret_cast<float*>(p + runs_bytes + part_bytes);
   }
   return w;
 }
@@ -1280,6 +1280,38 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
   const float scale_log2 = cfg->scale * 1.4426950408889634f;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
     const int G = cfg->n_q_heads / cfg->n_kv_heads;
+    // A table so narrow that one cluster per (sequence, KV head), all clusters
+    // on the GPU at once, has few units for each block: one launch.
+    const int64_t heads = int64_t(cfg->batch) * cfg->n_kv_heads;
+    const int64_t slots = int64_t(cache->max_pages) * cache->page_size;
+    const int64_t units = (slots + pdec::Tile<T, D>::kUnit - 1) / pdec::Tile<T, D>::kUnit;
+    int nc = 1;
+    while (nc < pdec::kMaxC && nc < units && 2 * nc * heads <= pdec::kBlocks) nc *= 2;
+    if (heads <= pdec::kBlocks && units <= int64_t(nc) * pdec::kFewUnits) {
+      const size_t smem = pdec::few_bytes<T, D>(G, accumulate != 0);
+      hga_status_t e = ensure_smem(
+          reinterpret_cast<const void*>(&pdec::paged_decode_few_kernel<T, D>), smem);
+      if (e != HGA_OK) return e;
+      return traced_launch(HGA_K_PAGED_DECODE, s, [&] {
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
+        lc.blockDim = dim3(pdec::kThreads);
+        lc.dynamicSmemBytes = smem;
+        lc.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(nc);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 2;
+        return cudaLaunchKernelEx(&lc, pdec::paged_decode_few_kernel<T, D>, view,
+                                  static_cast<const T*>(q), n_slots, G, int(accumulate),
+                                  scale_log2, static_cast<T*>(o), lse);
+      });
+    }
     const pdec::Work work = paged_work(cfg, cache, accumulate != 0, workspace).work;
     hga_status_t e = traced_launch(HGA_K_PAGED_DECODE, s, [&] {
       return launch_pdl(pdec::paged_decode_kernel<T, D>, dim3(pdec::kBlocks), dim3(pdec::kThreads),
@@ -1287,11 +1319,10 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
           static_cast<T*>(o), lse, work);
     });
     if (e != HGA_OK) return e;
-    const int joins = cfg->batch * cfg->n_q_heads;
-    dim3 grid(joins + (accumulate ? 4 * pdec::kBlocks : 0));
+    dim3 grid(pdec::kBlocks * (G + (accumulate ? 1 : 0)));
     return traced_launch(HGA_K_PAGED_JOIN, s, [&] {
       return launch_pdl(pdec::paged_join_kernel<T, D>, grid, dim3(pdec::kJoinThreads), 0, s, view,
-          n_slots, cfg->batch, G, joins, static_cast<T*>(o), lse, work);
+          n_slots, G, static_cast<T*>(o), lse, work);
     });
   });
 }

@@ -36,15 +36,21 @@
 // product is good to 2^-21, which plain tf32 (2^-11) is not.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
 
 namespace hga {
 namespace pdec {
 
-constexpr int kThreads = 256;
+// 12 warps on an SM: with 168 registers a thread a tile of K and of V and the
+// output stay in registers; 16 warps of 128 spill, and read 8 x 32768 slots
+// (bf16, d = 128) in 181 us instead of 168.  Small blocks, so that one merges
+// its warps while another reads.
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 2;
+constexpr int kBlocksPerSm = 3;
 constexpr int kBlocks = 148 * kBlocksPerSm;  // of the B200's 148 SMs
 constexpr int kMaxG = 8;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -67,9 +73,20 @@ struct Tile {
   static constexpr int kUnit = kWarps * kSlots;
 };
 
-// what the decode kernel leaves for the join kernel, at the head of the workspace
+// What a block of the decode kernel leaves for the join kernel: where its run
+// begins, and the head that begins in its last piece and goes on in the next
+// block's run (tail_units 0: none does)
+struct alignas(16) Run {
+  int64_t units;       // of the whole batch
+  int64_t seq_first;   // units before sequence `seq`
+  int64_t tail_first;  // units before the head
+  int32_t tail_units;  // units of the head
+  int32_t tail_head;   // sequence * n_kv_heads + head
+  int32_t seq;         // in which the run begins; -1: the block has no run
+};
+
 struct Work {
-  int64_t* first;   // [batch + 1]: units before each sequence; the last: all of them
+  Run* runs;        // [kBlocks]
   float* part;      // [2 * kBlocks][G * (D + 2)]: m[G], l[G], o[G][D] of an incomplete piece
   float* scores;    // [units][kUnit / kSlots][G][kSlots], in base 2; nullptr: not kept
 };
@@ -86,8 +103,8 @@ __device__ __forceinline__ int block_of(int64_t u, int64_t units, int blocks) {
 }
 // where block c puts the piece of a (sequence, head) that begins at unit u0:
 // its first piece is slot 0, its last slot 1
-__device__ __forceinline__ int part_slot(int c, int64_t u0, int64_t units, int blocks) {
-  return 2 * c + (u0 > run_begin(c, units, blocks) ? 1 : 0);
+__device__ __forceinline__ int part_slot(int c, int64_t u0, int64_t run_lo) {
+  return 2 * c + (u0 > run_lo ? 1 : 0);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -130,20 +147,22 @@ struct Acc {
   float m, l, o[L::kMt][4];
 };
 
-// Adds the tile in kr, vr.  live: slots of each slab that count (the others'
-// K and V registers hold 0).  out: where the scores go (nullptr: nowhere).
+// Scores of the tile in kr (base 2), by lane: heads lane / 4, two slots per
+// column of 8.  q: this lane's first piece of its query row.
 template <typename T, int D, typename KR>
-__device__ __forceinline__ void score_tile(const KR& kr, const uint4* qf, float scale_log2,
+__device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float scale_log2,
                                            float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2]) {
   using L = Tile<T, D>;
+  float acc[L::kSlabs][L::kNt][4] = {};
 #pragma unroll
-  for (int sl = 0; sl < L::kSlabs; ++sl)
+  for (int j = 0; j < L::kKc; ++j) {
+    const uint4 a = q[4 * j];
 #pragma unroll
-    for (int nt = 0; nt < L::kNt; ++nt) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int sl = 0; sl < L::kSlabs; ++sl)
 #pragma unroll
-      for (int j = 0; j < L::kKc; ++j) {
-        const uint4 k = kr[sl][nt][j], a = qf[j];
+      for (int nt = 0; nt < L::kNt; ++nt) {
+        float(&c)[4] = acc[sl][nt];
+        const uint4 k = kr[sl][nt][j];
         if constexpr (L::kBf16) {
           mma_bf16(c, a.x, 0u, a.y, 0u, k.x, k.y);
           mma_bf16(c, a.z, 0u, a.w, 0u, k.z, k.w);
@@ -157,11 +176,17 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* qf, float 
           mma_tf32(c, az.hi, 0u, aw.hi, 0u, kz.hi, kw.hi);
         }
       }
-      s[sl][nt][0] = c[0] * scale_log2;
-      s[sl][nt][1] = c[1] * scale_log2;
+  }
+#pragma unroll
+  for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+    for (int nt = 0; nt < L::kNt; ++nt) {
+      s[sl][nt][0] = acc[sl][nt][0] * scale_log2;
+      s[sl][nt][1] = acc[sl][nt][1] * scale_log2;
     }
 }
 
+// Adds the tile in vr, with its scores, to the running softmax.
 template <typename T, int D, typename VR>
 __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
                                          float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2],
@@ -241,13 +266,245 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
   }
 }
 
+// what a partial result (maximum m, sum l) counts in one with maximum M; one
+// that attended to nothing counts nothing
+__device__ __forceinline__ float part_scale(float m, float l, float M) {
+  return m == -INFINITY && l == 0.f ? 0.f : exp2f(m - M);
+}
+
+// the final output and log-sum-exp (base 2) of a sum
+template <typename T>
+__device__ __forceinline__ T final_out(float out, float sum) {
+  return from_float<T>(sum == 0.f ? 0.f : out / sum);
+}
+__device__ __forceinline__ float final_lse2(float M, float sum) {
+  return sum == 0.f ? -INFINITY : M + log2f(sum);
+}
+
+// The queries in shared memory: held in registers next to a tile of K and of
+// V and the output they would not fit.  Rows padded so that two rows' pieces
+// lie in different banks.
+template <typename T, int D>
+struct Queries {
+  alignas(16) T row[kMaxG][D + 64 / int(sizeof(T))];
+};
+
+// One block's share of a (sequence, KV head): its warps take the tiles of slots
+// [t_lo, t_hi) in turn, acc receives each warp's result.  q: the G query rows.
+// Slot t's scores go to score_out + (t / kSlots) * kSlots * G (nullptr: nowhere).
+template <typename T, int D>
+__device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __restrict__ table,
+                                       int h, const T* __restrict__ q, int G, int t_lo, int t_hi,
+                                       float scale_log2, float* score_out, Queries<T, D>& qs,
+                                       Acc<T, D>& acc) {
+  using L = Tile<T, D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n8 = lane >> 2, q4 = lane & 3;
+  constexpr int kPer = 16 / int(sizeof(T));  // elements of a 16-byte piece
+  const T* kh = static_cast<const T*>(cache.k) + (int64_t(h) << cache.page_shift) * D;
+  const T* vh = static_cast<const T*>(cache.v) + (int64_t(h) << cache.page_shift) * D;
+
+  // the G query rows, and rows of 0 up to 8 (the matrix instruction's)
+  for (int i = threadIdx.x; i < kMaxG * (D / kPer); i += kThreads) {
+    const int g = i / (D / kPer), e = i % (D / kPer) * kPer;
+    *reinterpret_cast<uint4*>(&qs.row[g][e]) =
+        g < G ? *reinterpret_cast<const uint4*>(q + g * D + e) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  acc.m = -INFINITY;
+  acc.l = 0.f;
+#pragma unroll
+  for (int t = 0; t < L::kMt; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc.o[t][i] = 0.f;
+
+  // The pages of this warp's slabs, 32 slabs at a time, one per lane (the
+  // next 32 on their way): a table lookup in front of every tile's loads
+  // would add its latency to each.
+  const int t_warp = t_lo + warp * L::kSlots;
+  auto page_ids = [&](int first) {  // of slabs first .. first + 31
+    const int k = first + lane;
+    const int s0 = t_warp + k / L::kSlabs * L::kUnit + k % L::kSlabs * L::kSlab;
+    return s0 < t_hi ? table[cache.page_of(s0)] : 0;
+  };
+  int ids = page_ids(0), next_ids = page_ids(32);
+  // of the tile at hand: how many slots of each slab count (0 on a page
+  // outside the pool), and its first row's offset
+  int live[L::kSlabs];
+  int64_t base[L::kSlabs];
+  auto locate = [&](int tile) {
+    const int t = t_warp + tile * L::kUnit, k = tile * L::kSlabs;
+    if (tile > 0 && k % 32 == 0) {
+      ids = next_ids;
+      next_ids = page_ids(k + 32);
+    }
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl) {
+      const int s0 = t + sl * L::kSlab;
+      const int page = __shfl_sync(0xffffffffu, ids, k % 32 + sl);
+      const bool ok = cache.has(page);
+      if (!ok && s0 < t_hi && lane == 0) latch_status(HGA_ERR_DEVICE_CHECK);
+      live[sl] = ok ? max(0, min(L::kSlab, t_hi - s0)) : 0;
+      base[sl] = int64_t(page) * cache.page_stride + int64_t(cache.row_of(s0)) * D;
+    }
+  };
+  uint4 kr[L::kSlabs][L::kNt][L::kKc], vr[L::kSlabs][L::kVt][L::kVc];
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto load_k = [&]() {
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+      for (int nt = 0; nt < L::kNt; ++nt) {
+        const uint4* src = reinterpret_cast<const uint4*>(kh + base[sl] + (nt * 8 + n8) * D);
+#pragma unroll
+        for (int j = 0; j < L::kKc; ++j)
+          kr[sl][nt][j] = nt * 8 + n8 < live[sl] ? __ldcs(src + q4 + 4 * j) : zero;
+      }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+      for (int r = 0; r < L::kVt; ++r) {
+        const int t = 2 * q4 + (r & 1) + 8 * (r >> 1);
+        const uint4* src = reinterpret_cast<const uint4*>(vh + base[sl] + t * D);
+#pragma unroll
+        for (int x = 0; x < L::kVc; ++x)
+          vr[sl][r][x] = t < live[sl] ? __ldcs(src + n8 + 8 * x) : zero;
+      }
+  };
+
+  const int tiles = t_warp < t_hi ? (t_hi - t_warp + L::kUnit - 1) / L::kUnit : 0;
+  if (tiles > 0) {
+    locate(0);
+    load_k();
+    load_v();
+  }
+  __syncthreads();
+  const uint4* qp = reinterpret_cast<const uint4*>(&qs.row[n8][0]) + q4;
+  for (int tile = 0; tile < tiles; ++tile) {
+    asm volatile("" : "+l"(qp));  // read again for every tile
+    float s[L::kSlabs][L::kNt][2];
+    score_tile<T, D>(kr, qp, scale_log2, s);
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+      for (int nt = 0; nt < L::kNt; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (nt * 8 + 2 * q4 + i >= live[sl]) s[sl][nt][i] = -INFINITY;
+    if (score_out && n8 < G) {
+      float* dst = score_out + int64_t(t_warp + tile * L::kUnit) * G + n8 * L::kSlots + 2 * q4;
+#pragma unroll
+      for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+        for (int nt = 0; nt < L::kNt; ++nt)
+          *reinterpret_cast<float2*>(dst + sl * L::kSlab + nt * 8) =
+              make_float2(s[sl][nt][0], s[sl][nt][1]);
+    }
+    // the next tile's K is requested before this tile's softmax, its V after
+    // the product that frees the registers
+    const bool more = tile + 1 < tiles;
+    if (more) {
+      locate(tile + 1);
+      load_k();
+    }
+    add_tile<T, D>(acc, vr, s, lane);
+    if (more) load_v();
+  }
+}
+
+// The warps' results into shared memory, then f(g, e, M, sum, out) for every
+// query head and element: the block's maximum, sum and output (relative to the
+// maximum), merged in warp order.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void merge_warps(const Acc<T, D>& acc, float (&wo)[kWarps][kMaxG][D],
+                                            float (&wm)[kWarps][kMaxG],
+                                            float (&wl)[kWarps][kMaxG], int G, F&& f) {
+  using L = Tile<T, D>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n8 = lane >> 2, q4 = lane & 3;
+  float l = acc.l;
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (q4 == 0) {
+    wm[warp][n8] = acc.m;
+    wl[warp][n8] = l;
+  }
+  {
+    constexpr int kPer = 16 / int(sizeof(T));  // elements of a 16-byte piece
+#pragma unroll
+    for (int x = 0; x < L::kVc; ++x)
+#pragma unroll
+      for (int w = 0; w < kPer / 2; ++w) {
+        const float(&c)[4] = acc.o[x * (kPer / 2) + w];
+        const int e = kPer * (n8 + 8 * x) + 2 * w;
+        *reinterpret_cast<float2*>(&wo[warp][2 * q4][e]) = make_float2(c[0], c[2]);
+        *reinterpret_cast<float2*>(&wo[warp][2 * q4 + 1][e]) = make_float2(c[1], c[3]);
+      }
+  }
+  __syncthreads();
+  for (int i = tid; i < G * D; i += kThreads) {
+    const int g = i / D, e = i % D;
+    float M = -INFINITY, sum = 0.f, out = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][g]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = part_scale(wm[w][g], wl[w][g], M);
+      sum = fmaf(a, wl[w][g], sum);
+      out = fmaf(a, wo[w][g][e], out);
+    }
+    f(g, e, M, sum, out);
+  }
+}
+
+// weight[slot] += sum_g 2^(s_g - lse_g) of slots [t_lo, t_hi), by the whole
+// block; scores as attend() stored them, lse in base 2 (+inf: no weight).  An
+// addition in memory, not a load and a store: two sequences may share a page.
+template <typename T, int D>
+__device__ __forceinline__ void add_weights(const PagedView& cache,
+                                            const int32_t* __restrict__ table, int h, int G,
+                                            int t_lo, int t_hi, const float* score,
+                                            const float* lse) {
+  using L = Tile<T, D>;
+  // four slots at a time: they lie on one page, and their records on 16 bytes
+#pragma unroll 2
+  for (int t = t_lo + 4 * int(threadIdx.x); t < t_hi; t += 4 * int(blockDim.x)) {
+    const int page = table[cache.page_of(t)];
+    if (!cache.has(page)) continue;
+    const float* s = score + int64_t(t / L::kSlots) * L::kSlots * G + t % L::kSlots;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < G; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(s + g * L::kSlots);
+      w.x += exp2f(x.x - lse[g]);
+      w.y += exp2f(x.y - lse[g]);
+      w.z += exp2f(x.z - lse[g]);
+      w.w += exp2f(x.w - lse[g]);
+    }
+    float* dst = &cache.weight[cache.record(page, h, cache.row_of(t))];
+    if (t + 4 <= t_hi) {
+      atomicAdd(reinterpret_cast<float4*>(dst), w);
+    } else {  // slots behind the last one stay as they are
+      atomicAdd(dst, w.x);
+      if (t + 1 < t_hi) atomicAdd(dst + 1, w.y);
+      if (t + 2 < t_hi) atomicAdd(dst + 2, w.z);
+    }
+  }
+}
+
 template <typename T, int D>
 struct Shared {
+  Queries<T, D> q;
   float wo[kWarps][kMaxG][D];
   float wm[kWarps][kMaxG], wl[kWarps][kMaxG];
   int64_t scan[kWarps];
-  int64_t seq_first;  // units before the sequence in which the block's run begins
-  int seq;
+  // the block's place in its run and the piece at hand: kept here rather than
+  // in registers, which the tiles need
+  int64_t run_lo, u, run_hi;  // the run, and its next unit
+  int64_t seq_first;     // units before sequence `seq`
+  int64_t part;          // where the partial result goes; -1: the piece is whole
+  int64_t score;         // first score of the head
+  int seq, head, t_lo, t_hi;
 };
 
 // grid kBlocks
@@ -259,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   using L = Tile<T, D>;
   __shared__ Shared<T, D> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n8 = lane >> 2, q4 = lane & 3;
   const int n_kv = cache.n_kv_heads;
   pdl_wait();
   pdl_launch_dependents();
@@ -294,14 +550,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     if (w < warp) before += sh.scan[w];
     units += sh.scan[w];
   }
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      work.first[b] = at;
-      at += units_of(b);
-    }
-    if (tid == 0) work.first[batch] = units;
-  }
   // idle sequences have no unit: nothing to attend to
   for (int b = blockIdx.x; b < batch; b += kBlocks) {
     if (n_slots[b] != 0) continue;
@@ -311,294 +559,318 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int i = tid; i < n_kv * G; i += kThreads) lse[row + i] = -INFINITY;
   }
   const int blocks = blocks_for(units);
-  if (int(blockIdx.x) >= blocks) return;
+  if (int(blockIdx.x) >= blocks) {
+    if (tid == 0) work.runs[blockIdx.x] = {units, 0, 0, 0, 0, -1};
+    return;
+  }
   const int64_t run_lo = run_begin(blockIdx.x, units, blocks);
-  const int64_t run_hi = run_begin(blockIdx.x + 1, units, blocks);
-  if (before <= run_lo && run_lo < before + mine) {
+  if (before <= run_lo && run_lo < before + mine) {  // one thread: its sequences hold run_lo
     int64_t at = before;
     int b = b_lo;
     while (run_lo >= at + units_of(b)) at += units_of(b++);
+    sh.run_lo = sh.u = run_lo;
+    sh.run_hi = run_begin(blockIdx.x + 1, units, blocks);
     sh.seq = b;
     sh.seq_first = at;
+    work.runs[blockIdx.x] = {units, at, 0, 0, 0, b};
   }
-  __syncthreads();
-  int b = sh.seq;
-  int64_t seq_first = sh.seq_first;
 
   // ---- its pieces -----------------------------------------------------------
-  for (int64_t u = run_lo; u < run_hi;) {
-    int64_t seq_units = units_of(b);
-    while (u >= seq_first + seq_units) {
-      seq_first += seq_units;
-      seq_units = units_of(++b);
-    }
-    const int n = n_slots[b];
-    const int head_units = int(seq_units / n_kv);
-    const int h = int((u - seq_first) / head_units);
-    const int64_t head_first = seq_first + int64_t(h) * head_units;
-    const int64_t u_end = min(run_hi, head_first + head_units);
-    const int t_lo = int(u - head_first) * L::kUnit;
-    const int t_hi = int(min(int64_t(n), (u_end - head_first) * L::kUnit));
-    const int64_t row0 = (int64_t(b) * n_kv + h) * G;
-    const int32_t* table = cache.table + int64_t(b) * cache.max_pages;
-    const T* kh = static_cast<const T*>(cache.k) + (int64_t(h) << cache.page_shift) * D;
-    const T* vh = static_cast<const T*>(cache.v) + (int64_t(h) << cache.page_shift) * D;
-    float* score_out = work.scores ? work.scores + head_first * L::kUnit * G : nullptr;
-
-    uint4 qf[L::kKc];
-#pragma unroll
-    for (int j = 0; j < L::kKc; ++j) {
-      qf[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (n8 < G)
-        qf[j] = *reinterpret_cast<const uint4*>(
-            reinterpret_cast<const char*>(q + (row0 + n8) * D) + 16 * (q4 + 4 * j));
-    }
-    Acc<T, D> acc;
-    acc.m = -INFINITY;
-    acc.l = 0.f;
-#pragma unroll
-    for (int t = 0; t < L::kMt; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc.o[t][i] = 0.f;
-
-    // first slot of each slab of the tile at hand, how many of its slots
-    // count (0 on a page outside the pool), and its first row's offset
-    int live[L::kSlabs];
-    int64_t base[L::kSlabs];
-    auto locate = [&](int t) {
-#pragma unroll
-      for (int sl = 0; sl < L::kSlabs; ++sl) {
-        const int s0 = t + sl * L::kSlab;
-        live[sl] = max(0, min(L::kSlab, t_hi - s0));
-        base[sl] = 0;
-        if (live[sl] > 0) {
-          const int page = table[cache.page_of(s0)];
-          if (!cache.has(page)) {
-            live[sl] = 0;
-            if (lane == 0) latch_status(HGA_ERR_DEVICE_CHECK);
-          } else {
-            base[sl] = int64_t(page) * cache.page_stride + int64_t(cache.row_of(s0)) * D;
-          }
-        }
+  while (true) {
+    __syncthreads();  // also: the next piece overwrites the warps' results
+    if (tid == 0 && sh.u < sh.run_hi) {
+      const int64_t u = sh.u;
+      int b = sh.seq;
+      int64_t seq_first = sh.seq_first, seq_units = units_of(b);
+      while (u >= seq_first + seq_units) {
+        seq_first += seq_units;
+        seq_units = units_of(++b);
       }
-    };
-    uint4 kr[L::kSlabs][L::kNt][L::kKc], vr[L::kSlabs][L::kVt][L::kVc];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    auto load_k = [&]() {
-#pragma unroll
-      for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-        for (int nt = 0; nt < L::kNt; ++nt) {
-          const uint4* src = reinterpret_cast<const uint4*>(kh + base[sl] + (nt * 8 + n8) * D);
-#pragma unroll
-          for (int j = 0; j < L::kKc; ++j)
-            kr[sl][nt][j] = nt * 8 + n8 < live[sl] ? __ldcs(src + q4 + 4 * j) : zero;
-        }
-    };
-    auto load_v = [&]() {
-#pragma unroll
-      for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-        for (int r = 0; r < L::kVt; ++r) {
-          const int t = 2 * q4 + (r & 1) + 8 * (r >> 1);
-          const uint4* src = reinterpret_cast<const uint4*>(vh + base[sl] + t * D);
-#pragma unroll
-          for (int x = 0; x < L::kVc; ++x)
-            vr[sl][r][x] = t < live[sl] ? __ldcs(src + n8 + 8 * x) : zero;
-        }
-    };
-
-    int t = t_lo + warp * L::kSlots;
-    if (t < t_hi) {
-      locate(t);
-      load_k();
-      load_v();
-    }
-    while (t < t_hi) {
-      float s[L::kSlabs][L::kNt][2];
-      score_tile<T, D>(kr, qf, scale_log2, s);
-#pragma unroll
-      for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-        for (int nt = 0; nt < L::kNt; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (nt * 8 + 2 * q4 + i >= live[sl]) s[sl][nt][i] = -INFINITY;
-      if (score_out && n8 < G) {
-        float* dst = score_out + int64_t(t) * G + n8 * L::kSlots + 2 * q4;
-#pragma unroll
-        for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-          for (int nt = 0; nt < L::kNt; ++nt)
-            *reinterpret_cast<float2*>(dst + sl * L::kSlab + nt * 8) =
-                make_float2(s[sl][nt][0], s[sl][nt][1]);
+      const int head_units = int(seq_units / n_kv);
+      const int h = int((u - seq_first) / head_units);
+      const int64_t head_first = seq_first + int64_t(h) * head_units;
+      const int64_t u_end = min(sh.run_hi, head_first + head_units);
+      const bool begins = u == head_first, ends = u_end == head_first + head_units;
+      if (begins && !ends) {
+        Run* run = work.runs + blockIdx.x;
+        run->tail_first = head_first;
+        run->tail_units = head_units;
+        run->tail_head = b * n_kv + h;
       }
-      // the next tile's K is requested before this tile's softmax, its V after
-      // the product that frees the registers
-      t += L::kUnit;
-      if (t < t_hi) {
-        locate(t);
-        load_k();
-      }
-      add_tile<T, D>(acc, vr, s, lane);
-      if (t < t_hi) load_v();
-    }
-
-    // ---- the warps' results, in warp order --------------------------------
-    float l = acc.l;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (q4 == 0) {
-      sh.wm[warp][n8] = acc.m;
-      sh.wl[warp][n8] = l;
-    }
-    {
-      constexpr int kPer = 16 / int(sizeof(T));  // elements of a 16-byte piece
-#pragma unroll
-      for (int x = 0; x < L::kVc; ++x)
-#pragma unroll
-        for (int w = 0; w < kPer / 2; ++w) {
-          const float(&c)[4] = acc.o[x * (kPer / 2) + w];
-          const int e = kPer * (n8 + 8 * x) + 2 * w;
-          *reinterpret_cast<float2*>(&sh.wo[warp][2 * q4][e]) = make_float2(c[0], c[2]);
-          *reinterpret_cast<float2*>(&sh.wo[warp][2 * q4 + 1][e]) = make_float2(c[1], c[3]);
-        }
+      sh.seq = b;
+      sh.seq_first = seq_first;
+      sh.head = h;
+      sh.t_lo = int(u - head_first) * L::kUnit;
+      sh.t_hi = int(min(int64_t(n_slots[b]), (u_end - head_first) * L::kUnit));
+      sh.part = begins && ends ? -1
+                               : part_slot(blockIdx.x, head_first, sh.run_lo) * int64_t(G) * (D + 2);
+      sh.score = head_first * L::kUnit * G;
+      sh.u = u_end;
+    } else if (tid == 0) {
+      sh.head = -1;
     }
     __syncthreads();
-    const bool whole = u == head_first && u_end == head_first + head_units;
-    float* part = work.part +
-                  int64_t(part_slot(blockIdx.x, head_first, units, blocks)) * G * (D + 2);
-    for (int i = tid; i < G * D; i += kThreads) {
-      const int g = i / D, e = i % D;
-      float M = -INFINITY, sum = 0.f, out = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.wm[w][g]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = sh.wm[w][g] == -INFINITY && sh.wl[w][g] == 0.f ? 0.f
-                                                                        : exp2f(sh.wm[w][g] - M);
-        sum = fmaf(a, sh.wl[w][g], sum);
-        out = fmaf(a, sh.wo[w][g][e], out);
-      }
-      if (whole) {
-        o[(row0 + g) * D + e] = from_float<T>(sum == 0.f ? 0.f : out / sum);
-        if (e == 0) lse[row0 + g] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    if (sh.head < 0) break;
+    Acc<T, D> acc;
+    {
+      const int b = sh.seq, h = sh.head;
+      attend<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h,
+                   q + (int64_t(b) * n_kv + h) * G * D, G, sh.t_lo, sh.t_hi, scale_log2,
+                   work.scores ? work.scores + sh.score : nullptr, sh.q, acc);
+    }
+    const int64_t row0 = (int64_t(sh.seq) * n_kv + sh.head) * G;
+    merge_warps(acc, sh.wo, sh.wm, sh.wl, G, [&](int g, int e, float M, float sum, float out) {
+      if (sh.part < 0) {
+        o[(row0 + g) * D + e] = final_out<T>(out, sum);
+        if (e == 0) lse[row0 + g] = final_lse2(M, sum) * kLn2;
       } else {
-        part[2 * G + i] = out;
+        float* part = work.part + sh.part;
+        part[2 * G + g * D + e] = out;
         if (e == 0) {
           part[g] = M;
           part[G + g] = sum;
         }
       }
-    }
-    __syncthreads();  // the next piece overwrites the warps' results
-    u = u_end;
+    });
   }
 }
 
 // ---------------------------------------------------------------------------
-// Joins the incomplete pieces, and adds the weights.  Blocks [0, joins):
-// one per (sequence, query head), they merge the partial results in block
-// order.  The others (accumulate) share the units out among themselves again:
-// LSE of the G heads, then weight[slot] += sum_g 2^(s_g - LSE_g) from the
-// scores that the decode kernel left (in L2 for the most part).
+// Short caches in one launch: a cluster of nc blocks per (sequence, KV head),
+// each with at most kFewUnits units of its slots; partial results, and the
+// scores for the weights, stay in shared memory and are joined through it.
+// ---------------------------------------------------------------------------
+constexpr int kMaxC = 8;
+constexpr int kFewUnits = 4;
+
+template <typename T, int D>
+struct FewShared {
+  Queries<T, D> q;
+  float wo[kWarps][kMaxG][D];
+  float wm[kWarps][kMaxG], wl[kWarps][kMaxG];
+  float po[kMaxG][D], pm[kMaxG], pl[kMaxG];  // the block's partial result
+  float head_lse[kMaxG];
+};
+// dynamic shared memory: FewShared, then (accumulate) the scores of kFewUnits units
+template <typename T, int D>
+__host__ __device__ constexpr size_t few_bytes(int G, bool accumulate) {
+  return sizeof(FewShared<T, D>) +
+         (accumulate ? size_t(kFewUnits) * Tile<T, D>::kUnit * G * 4 : 0);
+}
+
+// grid (nc, n_kv_heads, batch) in clusters of (nc, 1, 1); the table holds at
+// most nc * kFewUnits units
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    paged_decode_few_kernel(PagedView cache, const T* __restrict__ q,
+                            const int32_t* __restrict__ n_slots, int G, int accumulate,
+                            float scale_log2, T* __restrict__ o, float* __restrict__ lse) {
+  using L = Tile<T, D>;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = int(cluster.block_rank()), nc = int(cluster.num_blocks());
+  extern __shared__ __align__(16) unsigned char few_raw[];
+  FewShared<T, D>& sh = *reinterpret_cast<FewShared<T, D>*>(few_raw);
+  float* scores = reinterpret_cast<float*>(few_raw + sizeof(FewShared<T, D>));
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  // the whole cluster reads the same count and leaves here
+  const int n = rank == 0 && h == 0 && tid == 0 ? checked_slots(cache, n_slots, b) : n_slots[b];
+  if (n < 0 || int64_t(n) > cache.capacity()) return;
+  const int64_t row0 = (int64_t(b) * cache.n_kv_heads + h) * G;
+  const int32_t* table = cache.table + int64_t(b) * cache.max_pages;
+  const int head_units = (n + L::kUnit - 1) / L::kUnit;
+  const int t_lo = rank * head_units / nc * L::kUnit;
+  const int t_hi = min(n, (rank + 1) * head_units / nc * L::kUnit);
+  Acc<T, D> acc;
+  attend<T, D>(cache, table, h, q + row0 * D, G, t_lo, t_hi, scale_log2,
+               accumulate ? scores - int64_t(t_lo) * G : nullptr, sh.q, acc);
+  merge_warps(acc, sh.wo, sh.wm, sh.wl, G, [&](int g, int e, float M, float sum, float out) {
+    sh.po[g][e] = out;
+    if (e == 0) {
+      sh.pm[g] = M;
+      sh.pl[g] = sum;
+    }
+  });
+  cluster.sync();
+
+  // every block joins its share of the output elements, in block order; a
+  // thread per query head forms the log-sum-exp for the weights
+  auto stats = [&](int g, float& M, float& sum) {
+    float m[kMaxC], l[kMaxC];
+    M = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxC; ++r)
+      if (r < nc) {
+        const FewShared<T, D>* peer = cluster.map_shared_rank(&sh, r);
+        m[r] = peer->pm[g];
+        l[r] = peer->pl[g];
+        M = fmaxf(M, m[r]);
+      }
+#pragma unroll
+    for (int r = 0; r < kMaxC; ++r)
+      if (r < nc) sum = fmaf(part_scale(m[r], l[r], M), l[r], sum);
+  };
+  for (int i = rank * kThreads + tid; i < G * D; i += nc * kThreads) {
+    const int g = i / D, e = i % D;
+    float M, sum, out = 0.f;
+    stats(g, M, sum);
+    for (int r = 0; r < nc; ++r) {
+      const FewShared<T, D>* peer = cluster.map_shared_rank(&sh, r);
+      out = fmaf(part_scale(peer->pm[g], peer->pl[g], M), peer->po[g][e], out);
+    }
+    o[(row0 + g) * D + e] = final_out<T>(out, sum);
+    if (e == 0) lse[row0 + g] = final_lse2(M, sum) * kLn2;
+  }
+  if (accumulate) {
+    if (tid < G) {
+      float M, sum;
+      stats(tid, M, sum);
+      sh.head_lse[tid] = sum == 0.f ? INFINITY : M + log2f(sum);
+    }
+    __syncthreads();
+    add_weights<T, D>(cache, table, h, G, t_lo, t_hi, scores - int64_t(t_lo) * G, sh.head_lse);
+  }
+  __syncthreads();
+  __threadfence();  // as at the end of paged_join_kernel
+  pdl_launch_dependents();
+  cluster.sync();  // no block leaves while another reads its results
+}
+
+// ---------------------------------------------------------------------------
+// Joins the incomplete pieces, and adds the weights.  At most one head goes on
+// from each block's run to the next, so blocks [0, kBlocks * G) join: block
+// (c, g) the pieces of query head g of the head that begins in block c's last
+// piece, in block order.  The others (accumulate; one per block of the decode
+// kernel, over the same run) form the LSE of the G heads and add
+// sum_g 2^(s_g - LSE_g) to the weights from the scores that the decode kernel
+// left, in L2 for the most part.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// (m, l) over the pieces of a (sequence, head), for head g: by one warp
-__device__ __forceinline__ void join_stats(const Work& work, int G, int stride, int c0, int c1,
-                                           int64_t head_first, int64_t units, int blocks, int g,
-                                           int lane, float& M, float& sum) {
+// The pieces of a (sequence, head) that are joined: partial results first,
+// first + step, ...  Only the first block can have it as its last piece (see
+// part_slot), so one division finds them all.
+struct Pieces {
+  const float* first;
+  const float* rest;  // of the second piece
+  int64_t step;
+  int n;
+  __device__ __forceinline__ Pieces(const Work& work, int G, int d, int64_t head_first,
+                                    int head_units, int64_t units, int blocks) {
+    const int c0 = block_of(head_first, units, blocks);
+    n = block_of(head_first + head_units - 1, units, blocks) - c0 + 1;
+    const int64_t size = int64_t(G) * (d + 2);
+    step = 2 * size;
+    first = work.part + part_slot(c0, head_first, run_begin(c0, units, blocks)) * size;
+    rest = work.part + 2 * int64_t(c0 + 1) * size;
+  }
+  __device__ __forceinline__ const float* operator[](int i) const {
+    return i == 0 ? first : rest + (i - 1) * step;
+  }
+};
+
+// maximum and sum over the pieces for head g, by one warp; scale[i] (if not
+// nullptr) receives what piece i counts
+__device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, int lane, float& M,
+                                           float& sum, float* scale) {
+  constexpr int kHeld = (kBlocks + 31) / 32;
+  float m[kHeld], l[kHeld];
   M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    M = fmaxf(M, work.part[int64_t(part_slot(c, head_first, units, blocks)) * stride + g]);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const bool in = i * 32 + lane < pieces.n;
+    m[i] = in ? pieces[i * 32 + lane][g] : -INFINITY;
+    l[i] = in ? pieces[i * 32 + lane][G + g] : 0.f;
+    if (i * 32 >= pieces.n) break;
+    M = fmaxf(M, m[i]);
+  }
 #pragma unroll
   for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
   sum = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float* p = work.part + int64_t(part_slot(c, head_first, units, blocks)) * stride;
-    if (p[g] == -INFINITY && p[G + g] == 0.f) continue;
-    sum = fmaf(exp2f(p[g] - M), p[G + g], sum);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (i * 32 >= pieces.n) break;
+    const float a = part_scale(m[i], l[i], M);
+    sum = fmaf(a, l[i], sum);
+    if (scale && i * 32 + lane < pieces.n) scale[i * 32 + lane] = a;
   }
 #pragma unroll
   for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
-    paged_join_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int batch, int G,
-                      int joins, T* __restrict__ o, float* __restrict__ lse, Work work) {
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    paged_join_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int G,
+                      T* __restrict__ o, float* __restrict__ lse, Work work) {
   using L = Tile<T, D>;
   constexpr int kRows = kJoinThreads / D;
   __shared__ float red[kRows][D];
+  __shared__ float scale[kBlocks], total;
   __shared__ float head_lse[kMaxG];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_kv = cache.n_kv_heads;
-  const int stride = G * (D + 2);
   pdl_wait();
-  const int64_t units = work.first[batch];
-  const int blocks = blocks_for(units);
-  if (int(blockIdx.x) < joins) {
-    const int64_t row = blockIdx.x;
-    const int b = int(row / (n_kv * G)), h = int(row / G % n_kv), g = int(row % G);
-    const int head_units = int((work.first[b + 1] - work.first[b]) / n_kv);
-    if (head_units > 0) {
-      const int64_t head_first = work.first[b] + int64_t(h) * head_units;
-      const int c0 = block_of(head_first, units, blocks);
-      const int c1 = block_of(head_first + head_units - 1, units, blocks);
-      if (c0 < c1) {
+  if (int(blockIdx.x) < kBlocks * G) {
+    const int g = int(blockIdx.x) / kBlocks;
+    const Run run = work.runs[blockIdx.x % kBlocks];
+    if (run.tail_units > 0) {
+      const int64_t row = int64_t(run.tail_head) * G + g;
+      const Pieces pieces(work, G, D, run.tail_first, run.tail_units, run.units,
+                          blocks_for(run.units));
+      if (warp == 0) {
         float M, sum;
-        join_stats(work, G, stride, c0, c1, head_first, units, blocks, g, lane, M, sum);
-        const int e = tid % D, r = tid / D;
-        float out = 0.f;
+        join_stats(pieces, G, g, lane, M, sum, scale);
+        if (lane == 0) {
+          total = sum;
+          lse[row] = final_lse2(M, sum) * kLn2;
+        }
+      }
+      __syncthreads();
+      const int e = tid % D, r = tid / D;
+      float out = 0.f;
 #pragma unroll 8
-        for (int c = c0 + r; c <= c1; c += kRows) {
-          const float* p = work.part + int64_t(part_slot(c, head_first, units, blocks)) * stride;
-          const float a = p[g] == -INFINITY && p[G + g] == 0.f ? 0.f : exp2f(p[g] - M);
-          out = fmaf(a, p[2 * G + g * D + e], out);
-        }
-        red[r][e] = out;
-        __syncthreads();
-        if (r == 0) {
+      for (int i = r; i < pieces.n; i += kRows)
+        out = fmaf(scale[i], pieces[i][2 * G + g * D + e], out);
+      red[r][e] = out;
+      __syncthreads();
+      if (r == 0) {
 #pragma unroll
-          for (int i = 1; i < kRows; ++i) out += red[i][e];
-          o[row * D + e] = from_float<T>(sum == 0.f ? 0.f : out / sum);
-          if (e == 0) lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
-        }
+        for (int i = 1; i < kRows; ++i) out += red[i][e];
+        o[row * D + e] = final_out<T>(out, total);
       }
     }
-  } else if (units > 0) {
-    const int n_add = int(gridDim.x) - joins, me = int(blockIdx.x) - joins;
-    const int adders = int(units < n_add ? units : n_add);
-    const int64_t run_hi = me < adders ? run_begin(me + 1, units, adders) : 0;
-    int64_t u = me < adders ? run_begin(me, units, adders) : 0;
-    int b = 0;
-    if (u < run_hi) {  // the sequence of unit u
-      int lo = 0, hi = batch - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (work.first[mid] <= u) lo = mid;
-        else hi = mid - 1;
-      }
-      b = lo;
-    }
+  } else {
+    const int c = int(blockIdx.x) - kBlocks * G;
+    const Run run = work.runs[c];
+    const int blocks = blocks_for(run.units);
+    const int64_t run_hi = run.seq >= 0 ? run_begin(c + 1, run.units, blocks) : 0;
+    int64_t u = run.seq >= 0 ? run_begin(c, run.units, blocks) : 0;
+    int64_t seq_first = run.seq_first;
+    int b = run.seq;
     while (u < run_hi) {
-      while (u >= work.first[b + 1]) ++b;
-      const int head_units = int((work.first[b + 1] - work.first[b]) / n_kv);
-      const int h = int((u - work.first[b]) / head_units);
-      const int64_t head_first = work.first[b] + int64_t(h) * head_units;
+      int n, head_units;
+      while (true) {
+        n = n_slots[b];
+        head_units = n > 0 && int64_t(n) <= cache.capacity() ? (n + L::kUnit - 1) / L::kUnit : 0;
+        if (u < seq_first + int64_t(head_units) * n_kv) break;
+        seq_first += int64_t(head_units) * n_kv;
+        ++b;
+      }
+      const int h = int((u - seq_first) / head_units);
+      const int64_t head_first = seq_first + int64_t(h) * head_units;
       const int64_t u_end = min(run_hi, head_first + head_units);
-      const int n = n_slots[b];
       const int t_lo = int(u - head_first) * L::kUnit;
       const int t_hi = int(min(int64_t(n), (u_end - head_first) * L::kUnit));
-      const int c0 = block_of(head_first, units, blocks);
-      const int c1 = block_of(head_first + head_units - 1, units, blocks);
+      const Pieces pieces(work, G, D, head_first, head_units, run.units, blocks);
       __syncthreads();
       if (warp < G) {
         float x;
-        if (c0 < c1) {
+        if (pieces.n > 1) {
           float M, sum;
-          join_stats(work, G, stride, c0, c1, head_first, units, blocks, warp, lane, M, sum);
+          join_stats(pieces, G, warp, lane, M, sum, nullptr);
           x = sum == 0.f ? INFINITY : M + log2f(sum);
         } else {
           x = lse[(int64_t(b) * n_kv + h) * G + warp] / kLn2;
@@ -607,17 +879,8 @@ __global__ void __launch_bounds__(kJoinThreads)
         if (lane == 0) head_lse[warp] = x;
       }
       __syncthreads();
-      const int32_t* table = cache.table + int64_t(b) * cache.max_pages;
-      const float* score = work.scores + head_first * L::kUnit * G;
-      for (int t = t_lo + tid; t < t_hi; t += kJoinThreads) {
-        const int page = table[cache.page_of(t)];
-        if (!cache.has(page)) continue;
-        const float* s = score + int64_t(t / L::kSlots) * L::kSlots * G + t % L::kSlots;
-        float w = 0.f;
-        for (int g = 0; g < G; ++g) w += exp2f(s[g * L::kSlots] - head_lse[g]);
-        // two sequences may share a page: an addition, not a store
-        atomicAdd(&cache.weight[cache.record(page, h, cache.row_of(t))], w);
-      }
+      add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
+                        work.scores + head_first * L::kUnit * G, head_lse);
       u = u_end;
     }
   }
