@@ -1201,7 +1201,8 @@ PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumul
   const int unit = bf16 ? (d == 128 ? pdec::Tile<__nv_bfloat16, 128>::kUnit
                                     : pdec::Tile<__nv_bfloat16, 64>::kUnit)
                         : (d == 128 ? pdec::Tile<float, 128>::kUnit : pdec::Tile<float, 64>::kUnit);
-  const size_t slots = (size_t(c->max_pages) * c->page_size + unit - 1) / unit * unit;
+  const size_t slots = ((size_t(c->max_pages) * c->page_size + unit - 1) / unit +
+                        pdec::kHeadUnits) * unit;
   const size_t score_bytes =
       accumulate ? align256(slots * cfg->batch * cfg->n_q_heads * 4) : 0;
   char* p = static_cast<char*>(base);

@@ -33,7 +33,7 @@
 // bf16 parts (high and remainder, 16 bits): one part alone would add an error
 // as large as the rounding of a bf16 output.  Float32 operands are split into
 // two tf32 parts and the three largest of the four products are summed: each
-// product is good to 2^-21, which plain tf32 (2^-11) is not.
+// product is good to 2^-19, where one part alone is good to 2^-9.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -91,6 +91,14 @@ struct Work {
   float* scores;    // [units][kUnit / kSlots][G][kSlots], in base 2; nullptr: not kept
 };
 
+// A piece costs about as much as kHeadUnits units on top of those it has (its
+// queries, its first pages and rows, its merge, all waited for in turn), so
+// each head counts that many more where the runs are cut: position p of a
+// head that begins at unit u0 is its unit p - u0 - kHeadUnits.  Without it a
+// block that gets many short sequences is the last to end: 64 sequences of 0
+// to 8190 slots take 186 us instead of 169.
+constexpr int kHeadUnits = 2;
+
 // blocks in use, the run of block c, and the block that holds unit u
 __host__ __device__ __forceinline__ int blocks_for(int64_t units) {
   return int(units < kBlocks ? units : kBlocks);
@@ -123,14 +131,21 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// x = hi + lo in two tf32 numbers (the first cut off, so that it never
-// overflows; an infinite x has no remainder)
+// x = hi + lo in two tf32 numbers of 11 bits.  hi is cut off (K, V: two
+// instructions, and it never overflows) or, nearest, rounded: with a remainder
+// of either sign in one factor, the products of two remainders, which are left
+// out, add up to nothing in the mean.  lo is rounded.  (With both factors cut
+// off 5 x 4099 slots come out 9.6e-7 off, and with lo cut off too 1.7e-6.)
 struct Split {
   uint32_t hi, lo;
-  __device__ __forceinline__ explicit Split(uint32_t x) {
+  __device__ __forceinline__ explicit Split(uint32_t x, bool nearest = false) {
     hi = x & 0xffffe000u;
+    if (nearest) {
+      const uint32_t up = (x + 0x1000u) & 0xffffe000u;
+      if ((up & 0x7f800000u) != 0x7f800000u) hi = up;
+    }
     const float rest = __uint_as_float(x) - __uint_as_float(hi);
-    lo = __float_as_uint((x & 0x7fffffffu) < 0x7f800000u ? rest : 0.f) & 0xffffe000u;
+    lo = (__float_as_uint(rest) + 0x1000u) & 0xffffe000u;
   }
 };
 
@@ -147,43 +162,61 @@ struct Acc {
   float m, l, o[L::kMt][4];
 };
 
+// The queries in shared memory: held in registers next to a tile of K and of
+// V and the output they would not fit.  Rows padded so that two rows' pieces
+// lie in different banks.  float32: split, the remainders kLo pieces behind.
+template <typename T, int D>
+struct Queries {
+  static constexpr int kParts = sizeof(T) == 2 ? 1 : 2;
+  static constexpr int kRow = D + 64 / int(sizeof(T));
+  static constexpr int kLo = kMaxG * kRow * int(sizeof(T)) / 16;
+  alignas(16) T row[kParts][kMaxG][kRow];
+};
+
 // Scores of the tile in kr (base 2), by lane: heads lane / 4, two slots per
 // column of 8.  q: this lane's first piece of its query row.
 template <typename T, int D, typename KR>
 __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float scale_log2,
                                            float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2]) {
   using L = Tile<T, D>;
-  float acc[L::kSlabs][L::kNt][4] = {};
+  // float32: the small products have sums of their own, which shortens the
+  // chain of dependent instructions to a third
+  constexpr int kSums = L::kBf16 ? 1 : 3;
+  float acc[L::kSlabs][L::kNt][kSums][4] = {};
 #pragma unroll
   for (int j = 0; j < L::kKc; ++j) {
     const uint4 a = q[4 * j];
+    const uint4 a_lo = L::kBf16 ? a : q[Queries<T, D>::kLo + 4 * j];
 #pragma unroll
     for (int sl = 0; sl < L::kSlabs; ++sl)
 #pragma unroll
       for (int nt = 0; nt < L::kNt; ++nt) {
-        float(&c)[4] = acc[sl][nt];
+        auto& c = acc[sl][nt];
         const uint4 k = kr[sl][nt][j];
         if constexpr (L::kBf16) {
-          mma_bf16(c, a.x, 0u, a.y, 0u, k.x, k.y);
-          mma_bf16(c, a.z, 0u, a.w, 0u, k.z, k.w);
+          mma_bf16(c[0], a.x, 0u, a.y, 0u, k.x, k.y);
+          mma_bf16(c[0], a.z, 0u, a.w, 0u, k.z, k.w);
         } else {
-          const Split ax(a.x), ay(a.y), az(a.z), aw(a.w), kx(k.x), ky(k.y), kz(k.z), kw(k.w);
-          mma_tf32(c, ax.lo, 0u, ay.lo, 0u, kx.hi, ky.hi);
-          mma_tf32(c, ax.hi, 0u, ay.hi, 0u, kx.lo, ky.lo);
-          mma_tf32(c, ax.hi, 0u, ay.hi, 0u, kx.hi, ky.hi);
-          mma_tf32(c, az.lo, 0u, aw.lo, 0u, kz.hi, kw.hi);
-          mma_tf32(c, az.hi, 0u, aw.hi, 0u, kz.lo, kw.lo);
-          mma_tf32(c, az.hi, 0u, aw.hi, 0u, kz.hi, kw.hi);
+          const Split kx(k.x), ky(k.y), kz(k.z), kw(k.w);
+          mma_tf32(c[0], a.x, 0u, a.y, 0u, kx.hi, ky.hi);
+          mma_tf32(c[1], a_lo.x, 0u, a_lo.y, 0u, kx.hi, ky.hi);
+          mma_tf32(c[2], a.x, 0u, a.y, 0u, kx.lo, ky.lo);
+          mma_tf32(c[0], a.z, 0u, a.w, 0u, kz.hi, kw.hi);
+          mma_tf32(c[1], a_lo.z, 0u, a_lo.w, 0u, kz.hi, kw.hi);
+          mma_tf32(c[2], a.z, 0u, a.w, 0u, kz.lo, kw.lo);
         }
       }
   }
 #pragma unroll
   for (int sl = 0; sl < L::kSlabs; ++sl)
 #pragma unroll
-    for (int nt = 0; nt < L::kNt; ++nt) {
-      s[sl][nt][0] = acc[sl][nt][0] * scale_log2;
-      s[sl][nt][1] = acc[sl][nt][1] * scale_log2;
-    }
+    for (int nt = 0; nt < L::kNt; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = acc[sl][nt][0][i];
+        if constexpr (!L::kBf16) x += acc[sl][nt][1][i] + acc[sl][nt][2][i];
+        s[sl][nt][i] = x * scale_log2;
+      }
 }
 
 // Adds the tile in vr, with its scores, to the running softmax.
@@ -249,7 +282,7 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
           mma_bf16(acc.o[x * 4 + w], a0, a1, a2, a3, hi[0], hi[1]);
         }
     } else {
-      const Split p0(__float_as_uint(p[0][0])), p1(__float_as_uint(p[0][1]));
+      const Split p0(__float_as_uint(p[0][0]), true), p1(__float_as_uint(p[0][1]), true);
 #pragma unroll
       for (int x = 0; x < L::kVc; ++x)
 #pragma unroll
@@ -281,14 +314,6 @@ __device__ __forceinline__ float final_lse2(float M, float sum) {
   return sum == 0.f ? -INFINITY : M + log2f(sum);
 }
 
-// The queries in shared memory: held in registers next to a tile of K and of
-// V and the output they would not fit.  Rows padded so that two rows' pieces
-// lie in different banks.
-template <typename T, int D>
-struct Queries {
-  alignas(16) T row[kMaxG][D + 64 / int(sizeof(T))];
-};
-
 // One block's share of a (sequence, KV head): its warps take the tiles of slots
 // [t_lo, t_hi) in turn, acc receives each warp's result.  q: the G query rows.
 // Slot t's scores go to score_out + (t / kSlots) * kSlots * G (nullptr: nowhere).
@@ -307,8 +332,14 @@ __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __
   // the G query rows, and rows of 0 up to 8 (the matrix instruction's)
   for (int i = threadIdx.x; i < kMaxG * (D / kPer); i += kThreads) {
     const int g = i / (D / kPer), e = i % (D / kPer) * kPer;
-    *reinterpret_cast<uint4*>(&qs.row[g][e]) =
-        g < G ? *reinterpret_cast<const uint4*>(q + g * D + e) : make_uint4(0u, 0u, 0u, 0u);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (g < G) x = *reinterpret_cast<const uint4*>(q + g * D + e);
+    if constexpr (!L::kBf16) {
+      const Split sx(x.x, true), sy(x.y, true), sz(x.z, true), sw(x.w, true);
+      *reinterpret_cast<uint4*>(&qs.row[1][g][e]) = make_uint4(sx.lo, sy.lo, sz.lo, sw.lo);
+      x = make_uint4(sx.hi, sy.hi, sz.hi, sw.hi);
+    }
+    *reinterpret_cast<uint4*>(&qs.row[0][g][e]) = x;
   }
   acc.m = -INFINITY;
   acc.l = 0.f;
@@ -380,7 +411,7 @@ __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __
     load_v();
   }
   __syncthreads();
-  const uint4* qp = reinterpret_cast<const uint4*>(&qs.row[n8][0]) + q4;
+  const uint4* qp = reinterpret_cast<const uint4*>(&qs.row[0][n8][0]) + q4;
   for (int tile = 0; tile < tiles; ++tile) {
     asm volatile("" : "+l"(qp));  // read again for every tile
     float s[L::kSlabs][L::kNt][2];
@@ -524,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   auto units_of = [&](int b) -> int64_t {
     const int n = n_slots[b];
     return n > 0 && int64_t(n) <= cache.capacity()
-               ? int64_t(n_kv) * ((n + L::kUnit - 1) / L::kUnit)
+               ? int64_t(n_kv) * ((n + L::kUnit - 1) / L::kUnit + kHeadUnits)
                : 0;
   };
   const int per = (batch + kThreads - 1) / kThreads;
@@ -586,31 +617,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         seq_first += seq_units;
         seq_units = units_of(++b);
       }
-      const int head_units = int(seq_units / n_kv);
-      const int h = int((u - seq_first) / head_units);
-      const int64_t head_first = seq_first + int64_t(h) * head_units;
-      const int64_t u_end = min(sh.run_hi, head_first + head_units);
-      const bool begins = u == head_first, ends = u_end == head_first + head_units;
-      if (begins && !ends) {
+      const int stride = int(seq_units / n_kv), h = int((u - seq_first) / stride);
+      const int64_t first = seq_first + int64_t(h) * stride + kHeadUnits;  // of the head's slots
+      const int64_t end = first + stride - kHeadUnits, u_end = min(sh.run_hi, end);
+      const int64_t u_lo = max(u, first);
+      const bool begins = u_lo == first, ends = u_end == end;
+      if (begins && !ends && u_lo < u_end) {
         Run* run = work.runs + blockIdx.x;
-        run->tail_first = head_first;
-        run->tail_units = head_units;
+        run->tail_first = first;
+        run->tail_units = stride - kHeadUnits;
         run->tail_head = b * n_kv + h;
       }
       sh.seq = b;
       sh.seq_first = seq_first;
       sh.head = h;
-      sh.t_lo = int(u - head_first) * L::kUnit;
-      sh.t_hi = int(min(int64_t(n_slots[b]), (u_end - head_first) * L::kUnit));
+      sh.t_lo = int(u_lo - first) * L::kUnit;
+      sh.t_hi = int(min(int64_t(n_slots[b]), (u_end - first) * L::kUnit));
       sh.part = begins && ends ? -1
-                               : part_slot(blockIdx.x, head_first, sh.run_lo) * int64_t(G) * (D + 2);
-      sh.score = head_first * L::kUnit * G;
+                               : part_slot(blockIdx.x, first, sh.run_lo) * int64_t(G) * (D + 2);
+      sh.score = first * L::kUnit * G;
       sh.u = u_end;
     } else if (tid == 0) {
       sh.head = -1;
     }
     __syncthreads();
     if (sh.head < 0) break;
+    if (sh.t_lo >= sh.t_hi) continue;  // the run ends before the head's first slot
     Acc<T, D> acc;
     {
       const int b = sh.seq, h = sh.head;
@@ -851,20 +883,24 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     int64_t seq_first = run.seq_first;
     int b = run.seq;
     while (u < run_hi) {
-      int n, head_units;
+      int n, stride;
       while (true) {
         n = n_slots[b];
-        head_units = n > 0 && int64_t(n) <= cache.capacity() ? (n + L::kUnit - 1) / L::kUnit : 0;
-        if (u < seq_first + int64_t(head_units) * n_kv) break;
-        seq_first += int64_t(head_units) * n_kv;
+        stride = n > 0 && int64_t(n) <= cache.capacity()
+                     ? (n + L::kUnit - 1) / L::kUnit + kHeadUnits
+                     : 0;
+        if (u < seq_first + int64_t(stride) * n_kv) break;
+        seq_first += int64_t(stride) * n_kv;
         ++b;
       }
-      const int h = int((u - seq_first) / head_units);
-      const int64_t head_first = seq_first + int64_t(h) * head_units;
-      const int64_t u_end = min(run_hi, head_first + head_units);
-      const int t_lo = int(u - head_first) * L::kUnit;
-      const int t_hi = int(min(int64_t(n), (u_end - head_first) * L::kUnit));
-      const Pieces pieces(work, G, D, head_first, head_units, run.units, blocks);
+      const int h = int((u - seq_first) / stride), head_units = stride - kHeadUnits;
+      const int64_t first = seq_first + int64_t(h) * stride + kHeadUnits;
+      const int64_t u_end = min(run_hi, first + head_units);
+      u = max(u, first);
+      if (u >= u_end) break;
+      const int t_lo = int(u - first) * L::kUnit;
+      const int t_hi = int(min(int64_t(n), (u_end - first) * L::kUnit));
+      const Pieces pieces(work, G, D, first, head_units, run.units, blocks);
       __syncthreads();
       if (warp < G) {
         float x;
@@ -880,7 +916,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       }
       __syncthreads();
       add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
-                        work.scores + head_first * L::kUnit * G, head_lse);
+                        work.scores + first * L::kUnit * G, head_lse);
       u = u_end;
     }
   }

@@ -556,7 +556,8 @@ HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hg
  *   weight[slot] += sum_g exp(s_gj - LSE_g).
  * n_slots[b] = 0: O = 0, LSE = -inf.  Slots on a page outside [0, n_pages)
  * are left out of the softmax.  Rows of the last page behind n_slots[b] are
- * never used, whatever they hold.  Deterministic (with accumulate = 1 as long
+ * never used, whatever they hold; keys and values of slots in use must be
+ * finite (others make their head's results NaN or undefined numbers).  Deterministic (with accumulate = 1 as long
  * as no two sequences share a page).  workspace: at least
  * hga_paged_decode_workspace_size() bytes of device memory, 16-byte aligned,
  * whose contents do not matter; not used by two calls at once.

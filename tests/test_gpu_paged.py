@@ -1,11 +1,14 @@
 """The paged cache's kernels against the float64 reference (paged_ref).
 
-Tolerances count what the kernels round.  Scores: a float32 sum of d products
-(for float32 inputs each product is at least 21 bits exact), so
-|ds| <= (2 d 2^-24 + 2^-21) * sum_e |q_e k_e| * scale.  A softmax weight is then
-off by at most the factor exp(2 ds) and a few steps of exp2, and the output by
-that times sum_s p_s |v_s| plus the float32 sum over n slots (n 2^-23), plus
-half a step of the output's type.
+Tolerances count what the kernels round.  Scores: a float32 sum of d products,
+so |ds| <= (2 d 2^-24 + product) * sum_e |q_e k_e| * scale.  A product of bf16
+numbers is exact; of float32 numbers each factor x = hi + lo + rest has
+|lo| < 2^-10 |x| (11 bits, cut off) and |rest| <= 2^-11 |lo| (the next 11,
+rounded), and lo * lo is left out, so it is off by at most
+2 * 2^-21 + 2^-20 = 2^-19.  A softmax weight is then off by at most the factor
+exp(2 ds) and a few steps of exp2 (2^-20), and the output by that, and by the
+same 2^-19 of each p v, times sum_s p_s |v_s|, plus the float32 sum over n
+slots (n 2^-23), plus half a step of the output's type.
 """
 
 import math
@@ -19,6 +22,7 @@ from hga_testlib import to_f64
 pytestmark = pytest.mark.gpu
 
 HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+PRODUCT = {"bf16": 0.0, "f32": 2.0 ** -19}
 
 
 class Case:
@@ -95,7 +99,7 @@ class Case:
         o, lse, w, reach, spread = ref.decode(to_f64(self.q), k, v, table, n, self.cfg.head_dim ** -0.5)
         got_o, got_lse = to_f64(self.o), self.lse.double().cpu().numpy()
         G = self.cfg.n_q_heads // self.cfg.n_kv_heads
-        ds = (2 * self.cfg.head_dim * 2.0 ** -24 + 2.0 ** -21) * reach      # [B, Hq]
+        ds = (2 * self.cfg.head_dim * 2.0 ** -24 + PRODUCT[self.dtype]) * reach      # [B, Hq]
         longest = max(n) if n else 0
         for b in range(self.cfg.batch):
             if b in skip:
@@ -108,7 +112,7 @@ class Case:
             assert ((got_lse[b] > -math.inf) == live).all()
             tol = HALF_STEP[self.dtype] * np.abs(o[b]) + \
                 (2 * ds[b][:, None] + 2.0 ** -15 * (self.dtype == "bf16") + 2.0 ** -20
-                 + n[b] * 2.0 ** -23) * spread[b]
+                 + PRODUCT[self.dtype] + n[b] * 2.0 ** -23) * spread[b]
             assert (np.abs(got_o[b] - o[b]) <= tol).all(), (b, np.abs(got_o[b] - o[b]).max())
             tol = ds[b] + 2.0 ** -20 * (1 + np.abs(lse[b])) + n[b] * 2.0 ** -23
             assert (np.abs(got_lse[b] - lse[b])[live] <= tol[live]).all(), b
@@ -203,7 +207,7 @@ def test_decode_slots_that_score_minus_infinity(dtype, low):
     sc = (k[pg, 0, row][left] @ np.full(128, 8.0)) / math.sqrt(128)
     p = np.exp(sc - sc.max())
     want = (p / p.sum()) @ v[pg, 0, row][left]
-    ds = (256 * 2.0 ** -24 + 2.0 ** -21) * (np.abs(k[pg, 0, row][left]).sum(1).max() * 8 / math.sqrt(128))
+    ds = (256 * 2.0 ** -24 + PRODUCT[dtype]) * (np.abs(k[pg, 0, row][left]).sum(1).max() * 8 / math.sqrt(128))
     spread = (p / p.sum()) @ np.abs(v[pg, 0, row][left])
     tol = HALF_STEP[dtype] * np.abs(want) + (2 * ds + 2.0 ** -14) * spread
     for g in range(2):
