@@ -37,7 +37,7 @@ EXPORTS = ("hga_version", "hga_status_string", "hga_last_cuda_error", "hga_build
            "hga_paged_append", "hga_paged_decode_workspace_size", "hga_paged_decode",
            "hga_paged_evict_workspace_size", "hga_paged_evict")
 HGA_NOALLOC_SCRATCH_BYTES = 4 << 20
-HGA_K_COUNT = 20
+HGA_K_COUNT = 21
 
 
 class HgaError(RuntimeError):

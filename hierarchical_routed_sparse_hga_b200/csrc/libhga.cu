@@ -834,7 +834,8 @@ const char* hga_kernel_name(int kind) {
       "attn_fwd_simt",  "attn_bwd_dq_simt",  "attn_bwd_dkdv_simt",  "attn_fwd_tc",
       "attn_bwd_dq_tc", "attn_bwd_dkdv_tc",  "tier_dedup",          "tier_copy",
       "route_fused",    "decode",            "query_summaries",     "prepare",
-      "paged_append",   "paged_decode",      "paged_join",          "paged_evict"};
+      "paged_append",   "paged_decode",      "paged_join",          "paged_evict",
+      "paged_move"};
   return (kind >= 0 && kind < HGA_K_COUNT) ? names[kind] : "unknown";
 }
 
@@ -1331,9 +1332,11 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
 extern "C" size_t hga_paged_evict_workspace_size(const hga_config_t* cfg,
                                                  const hga_pages_t* cache) {
   if (check_pages(cfg, cache) != HGA_OK) return 0;
-  // a (page, row) of every hole and mover: at most one entry per slot
-  return align256(size_t(cfg->batch) * cfg->n_kv_heads * cache->max_pages * cache->page_size *
-                  sizeof(int2));
+  // the numbers of holes and movers of every (sequence, head)'s blocks, then a
+  // (page, row) of every hole and mover: at most one entry per slot
+  const size_t heads = size_t(cfg->batch) * cfg->n_kv_heads;
+  return align256(heads * pev::kMaxC * sizeof(int2)) +
+         align256(heads * cache->max_pages * cache->page_size * sizeof(int2));
 }
 
 extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
@@ -1351,38 +1354,46 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   if (ws_bytes < hga_paged_evict_workspace_size(cfg, cache)) return HGA_ERR_WORKSPACE;
   const PagedView view = paged_view(cfg, cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // cluster size: enough blocks to fill the GPU about twice (four fit on an
-  // SM), but no share below 1024 slots of the table's width, where the
-  // cluster's barriers would cost more than the share
+  // cluster size: enough blocks to fill the GPU once (two fit on an SM), but
+  // no share below 128 slots of the table's width
   const int64_t heads = int64_t(cfg->batch) * cfg->n_kv_heads;
   const int64_t slots = int64_t(cache->max_pages) * cache->page_size;
   int nc = pev::kMaxC;
-  while (nc > 1 && (heads * nc > 2 * int64_t(sm_count()) || slots / nc < 1024)) nc /= 2;
-  const int key_cap = int(std::min<int64_t>(pev::kKeyCap, ((slots + nc - 1) / nc + 3) & ~int64_t(3)));
-  const size_t smem = size_t(key_cap) * 4;
+  while (nc > 1 && (heads * nc > 2 * int64_t(sm_count()) || slots / nc < 128)) nc /= 2;
+  const int key_cap =
+      int(std::min<int64_t>(pev::kKeyCap, ((slots + nc - 1) / nc + 3) & ~int64_t(3)));
+  const size_t smem = sizeof(pev::Shared) + size_t(key_cap) * 4;
+  int2* counts = static_cast<int2*>(workspace);
+  int2* moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) +
+                                        align256(size_t(heads) * pev::kMaxC * sizeof(int2)));
+  hga_status_t e = ensure_smem(reinterpret_cast<const void*>(&pev::paged_evict_kernel), smem);
+  if (e != HGA_OK) return e;
+  e = traced_launch(HGA_K_PAGED_EVICT, s, [&] {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
+    lc.blockDim = dim3(pev::kThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(nc);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, pev::paged_evict_kernel, view, n_slots, pos, int(keep),
+                              int(sinks), int(recent), key_cap, counts, moves);
+  });
+  if (e != HGA_OK) return e;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    // the limit counts the kernel's static shared memory too
-    hga_status_t e = ensure_smem(reinterpret_cast<const void*>(&pev::paged_evict_kernel<T, D>),
-                                 smem + sizeof(pev::Shared));
-    if (e != HGA_OK) return e;
-    return traced_launch(HGA_K_PAGED_EVICT, s, [&] {
-      cudaLaunchConfig_t lc = {};
-      lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
-      lc.blockDim = dim3(pev::kThreads);
-      lc.dynamicSmemBytes = smem;
-      lc.stream = s;
-      cudaLaunchAttribute attr[2];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = unsigned(nc);
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[1].val.programmaticStreamSerializationAllowed = 1;
-      lc.attrs = attr;
-      lc.numAttrs = 2;
-      return cudaLaunchKernelEx(&lc, pev::paged_evict_kernel<T, D>, view, n_slots, pos, int(keep),
-                                int(sinks), int(recent), key_cap,
-                                static_cast<int2*>(workspace));
+    // about eight blocks of moves on an SM, at least one per (sequence, head)
+    const int64_t x = std::max<int64_t>(1, 8 * int64_t(sm_count()) / heads);
+    dim3 grid(unsigned(std::min<int64_t>(x, (slots + 63) / 64)), cfg->n_kv_heads, cfg->batch);
+    return traced_launch(HGA_K_PAGED_MOVE, s, [&] {
+      return launch_pdl(pev::paged_move_kernel<T, D>, grid, dim3(pev::kMoveThreads), 0, s, view,
+                        n_slots, nc, counts, moves);
     });
   });
 }

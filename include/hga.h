@@ -637,7 +637,8 @@ typedef enum {
   HGA_K_PAGED_DECODE = 17,
   HGA_K_PAGED_JOIN = 18,
   HGA_K_PAGED_EVICT = 19,
-  HGA_K_COUNT = 20
+  HGA_K_PAGED_MOVE = 20,
+  HGA_K_COUNT = 21
 } hga_kernel_kind_t;
 
 /* Name of a kernel kind ("attn_fwd_simt", ...). */

@@ -198,6 +198,7 @@ def test_layer_finds_the_row_stride():
 
 
 def test_kernel_names():
-    assert [hga.hga_kernel_name(i) for i in range(16, 20)] == [
-        "paged_append", "paged_decode", "paged_join", "paged_evict"]
-    assert _lib.HGA_K_COUNT == 20
+    assert [hga.hga_kernel_name(i) for i in range(16, 21)] == [
+        "paged_append", "paged_decode", "paged_join", "paged_evict",
+        "paged_move"]
+    assert _lib.HGA_K_COUNT == 21
