@@ -1246,14 +1246,19 @@ extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_page
   if (s_new == 0) return HGA_OK;
   const PagedView view = paged_view(cfg, cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const double log2_base = rope_base > 1.f ? std::log2(double(rope_base)) : 0.0;
+  const double ratio = rope_base > 1.f ? std::pow(double(rope_base), -2.0 / cfg->head_dim) : 0.0;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    dim3 grid(s_new, cfg->batch);
+    // few tokens, less than four warps an SM: several share one
+    const int64_t tokens = int64_t(cfg->batch) * s_new;
+    if (tokens > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
+    const int per_tok = tokens <= 4 * int64_t(sm_count()) ? kTokenWarps : 1;
+    const int64_t blocks = (tokens * per_tok + kAppendWarps - 1) / kAppendWarps;
     return traced_launch(HGA_K_PAGED_APPEND, s, [&] {
-      return launch_pdl(paged_append_kernel<T, D>, grid, dim3(kAppendThreads), 0, s, view,
-          static_cast<const T*>(q_proj), static_cast<const T*>(k_proj),
-          static_cast<const T*>(v_proj), q_row_stride, kv_row_stride, s_new, n_new, n_slots, pos,
-          cfg->n_q_heads, log2_base, static_cast<T*>(q_out));
+      return launch_pdl(paged_append_kernel<T, D>, dim3(unsigned(blocks)),
+          dim3(32 * kAppendWarps), 0, s, view, static_cast<const T*>(q_proj),
+          static_cast<const T*>(k_proj), static_cast<const T*>(v_proj), q_row_stride,
+          kv_row_stride, int(tokens), int(s_new), per_tok, n_new, n_slots, pos,
+          int(cfg->n_q_heads), ratio, static_cast<T*>(q_out));
     });
   });
 }
@@ -1321,10 +1326,11 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
           static_cast<T*>(o), lse, work);
     });
     if (e != HGA_OK) return e;
-    dim3 grid(pdec::kBlocks * (G + (accumulate ? 1 : 0)));
+    const int adders = accumulate ? pdec::kBlocks : 0;
+    dim3 grid(pdec::kBlocks * G + adders);
     return traced_launch(HGA_K_PAGED_JOIN, s, [&] {
       return launch_pdl(pdec::paged_join_kernel<T, D>, grid, dim3(pdec::kJoinThreads), 0, s, view,
-          n_slots, G, static_cast<T*>(o), lse, work);
+          n_slots, G, adders, static_cast<T*>(o), lse, work);
     });
   });
 }
@@ -1388,8 +1394,9 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   });
   if (e != HGA_OK) return e;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    // about eight blocks of moves on an SM, at least one per (sequence, head)
-    const int64_t x = std::max<int64_t>(1, 8 * int64_t(sm_count()) / heads);
+    // one wave: four blocks of moves fit on an SM (8 x 32768 slots cut to 8192:
+    // 108 us, with eight 110, with six 120); at least one per (sequence, head)
+    const int64_t x = std::max<int64_t>(1, 4 * int64_t(sm_count()) / heads);
     dim3 grid(unsigned(std::min<int64_t>(x, (slots + 63) / 64)), cfg->n_kv_heads, cfg->batch);
     return traced_launch(HGA_K_PAGED_MOVE, s, [&] {
       return launch_pdl(pev::paged_move_kernel<T, D>, grid, dim3(pev::kMoveThreads), 0, s, view,

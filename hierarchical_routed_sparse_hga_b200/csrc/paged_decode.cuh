@@ -772,13 +772,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 }
 
 // ---------------------------------------------------------------------------
-// Joins the incomplete pieces, and adds the weights.  At most one head goes on
-// from each block's run to the next, so blocks [0, kBlocks * G) join: block
-// (c, g) the pieces of query head g of the head that begins in block c's last
-// piece, in block order.  The others (accumulate; one per block of the decode
-// kernel, over the same run) form the LSE of the G heads and add
-// sum_g 2^(s_g - LSE_g) to the weights from the scores that the decode kernel
-// left, in L2 for the most part.
+// Joins the incomplete pieces, and adds the weights.  The first `adders` blocks
+// (accumulate: kBlocks, one per block of the decode kernel, over the same run;
+// else 0) form the LSE of the G heads and add sum_g 2^(s_g - LSE_g) to the
+// weights from the scores that the decode kernel left, in L2 for the most part.
+// At most one head goes on from each block's run to the next, so the other
+// kBlocks * G blocks join: block (c, g) the pieces of query head g of the head
+// that begins in block c's last piece, in block order.  Most of them have
+// nothing to do; the adders come first so as not to wait for them.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
@@ -835,7 +836,7 @@ __device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, i
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 4)
-    paged_join_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int G,
+    paged_join_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int G, int adders,
                       T* __restrict__ o, float* __restrict__ lse, Work work) {
   using L = Tile<T, D>;
   constexpr int kRows = kJoinThreads / D;
@@ -845,41 +846,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_kv = cache.n_kv_heads;
   pdl_wait();
-  if (int(blockIdx.x) < kBlocks * G) {
-    const int g = int(blockIdx.x) / kBlocks;
-    const Run run = work.runs[blockIdx.x % kBlocks];
-    if (run.tail_units > 0) {
-      const int64_t row = int64_t(run.tail_head) * G + g;
-      const Pieces pieces(work, G, D, run.tail_first, run.tail_units, run.units,
-                          blocks_for(run.units));
-      if (warp == 0) {
-        float M, sum;
-        join_stats(pieces, G, g, lane, M, sum, scale);
-        if (lane == 0) {
-          total = sum;
-          lse[row] = final_lse2(M, sum) * kLn2;
-        }
-      }
-      __syncthreads();
-      const int e = tid % D, r = tid / D;
-      float out = 0.f;
-#pragma unroll 8
-      for (int i = r; i < pieces.n; i += kRows)
-        out = fmaf(scale[i], pieces[i][2 * G + g * D + e], out);
-      red[r][e] = out;
-      __syncthreads();
-      if (r == 0) {
-#pragma unroll
-        for (int i = 1; i < kRows; ++i) out += red[i][e];
-        o[row * D + e] = final_out<T>(out, total);
-      }
-    }
-  } else {
-    const int c = int(blockIdx.x) - kBlocks * G;
+  if (int(blockIdx.x) < adders) {
+    const int c = int(blockIdx.x);
     const Run run = work.runs[c];
+    if (run.seq < 0) return;
     const int blocks = blocks_for(run.units);
-    const int64_t run_hi = run.seq >= 0 ? run_begin(c + 1, run.units, blocks) : 0;
-    int64_t u = run.seq >= 0 ? run_begin(c, run.units, blocks) : 0;
+    int64_t u = run_begin(c, run.units, blocks);
+    const int64_t run_hi = run_begin(c + 1, run.units, blocks);
     int64_t seq_first = run.seq_first;
     int b = run.seq;
     while (u < run_hi) {
@@ -918,6 +891,34 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
                         work.scores + first * L::kUnit * G, head_lse);
       u = u_end;
+    }
+  } else {
+    const int g = (int(blockIdx.x) - adders) / kBlocks;
+    const Run run = work.runs[(int(blockIdx.x) - adders) % kBlocks];
+    if (run.tail_units == 0) return;
+    const int64_t row = int64_t(run.tail_head) * G + g;
+    const Pieces pieces(work, G, D, run.tail_first, run.tail_units, run.units,
+                        blocks_for(run.units));
+    if (warp == 0) {
+      float M, sum;
+      join_stats(pieces, G, g, lane, M, sum, scale);
+      if (lane == 0) {
+        total = sum;
+        lse[row] = final_lse2(M, sum) * kLn2;
+      }
+    }
+    __syncthreads();
+    const int e = tid % D, r = tid / D;
+    float out = 0.f;
+#pragma unroll 8
+    for (int i = r; i < pieces.n; i += kRows)
+      out = fmaf(scale[i], pieces[i][2 * G + g * D + e], out);
+    red[r][e] = out;
+    __syncthreads();
+    if (r == 0) {
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) out += red[i][e];
+      o[row * D + e] = final_out<T>(out, total);
     }
   }
   // the next kernel on the stream may read what this call wrote before its
