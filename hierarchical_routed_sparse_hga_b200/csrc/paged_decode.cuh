@@ -489,18 +489,18 @@ __device__ __forceinline__ void merge_warps(const Acc<T, D>& acc, float (&wo)[kW
   }
 }
 
-// weight[slot] += sum_g 2^(s_g - lse_g) of slots [t_lo, t_hi), by the whole
-// block; scores as attend() stored them, lse in base 2 (+inf: no weight).  An
+// weight[slot] += sum_g 2^(s_g - lse_g) of slots [t_lo, t_hi), by `threads`
+// threads; scores as attend() stored them, lse in base 2 (+inf: no weight).  An
 // addition in memory, not a load and a store: two sequences may share a page.
 template <typename T, int D>
 __device__ __forceinline__ void add_weights(const PagedView& cache,
                                             const int32_t* __restrict__ table, int h, int G,
                                             int t_lo, int t_hi, const float* score,
-                                            const float* lse) {
+                                            const float* lse, int thread, int threads) {
   using L = Tile<T, D>;
   // four slots at a time: they lie on one page, and their records on 16 bytes
 #pragma unroll 2
-  for (int t = t_lo + 4 * int(threadIdx.x); t < t_hi; t += 4 * int(blockDim.x)) {
+  for (int t = t_lo + 4 * thread; t < t_hi; t += 4 * threads) {
     const int page = table[cache.page_of(t)];
     if (!cache.has(page)) continue;
     const float* s = score + int64_t(t / L::kSlots) * L::kSlots * G + t % L::kSlots;
@@ -763,7 +763,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       sh.head_lse[tid] = sum == 0.f ? INFINITY : M + log2f(sum);
     }
     __syncthreads();
-    add_weights<T, D>(cache, table, h, G, t_lo, t_hi, scores - int64_t(t_lo) * G, sh.head_lse);
+    add_weights<T, D>(cache, table, h, G, t_lo, t_hi, scores - int64_t(t_lo) * G, sh.head_lse, tid,
+                      kThreads);
   }
   __syncthreads();
   __threadfence();  // as at the end of paged_join_kernel
@@ -805,33 +806,26 @@ struct Pieces {
   }
 };
 
-// maximum and sum over the pieces for head g, by one warp; scale[i] (if not
-// nullptr) receives what piece i counts
-__device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, int lane, float& M,
+// maximum and sum over the pieces for head g, by the kLanes lanes of a warp
+// that share it (sub: which of them); scale[i] (if not nullptr) receives what
+// piece i counts
+template <int kLanes>
+__device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, int sub, float& M,
                                            float& sum, float* scale) {
-  constexpr int kHeld = (kBlocks + 31) / 32;
-  float m[kHeld], l[kHeld];
   M = -INFINITY;
+#pragma unroll 4
+  for (int i = sub; i < pieces.n; i += kLanes) M = fmaxf(M, pieces[i][g]);
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const bool in = i * 32 + lane < pieces.n;
-    m[i] = in ? pieces[i * 32 + lane][g] : -INFINITY;
-    l[i] = in ? pieces[i * 32 + lane][G + g] : 0.f;
-    if (i * 32 >= pieces.n) break;
-    M = fmaxf(M, m[i]);
-  }
-#pragma unroll
-  for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  for (int w = kLanes / 2; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
   sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    if (i * 32 >= pieces.n) break;
-    const float a = part_scale(m[i], l[i], M);
-    sum = fmaf(a, l[i], sum);
-    if (scale && i * 32 + lane < pieces.n) scale[i * 32 + lane] = a;
+#pragma unroll 4
+  for (int i = sub; i < pieces.n; i += kLanes) {
+    const float l = pieces[i][G + g], a = part_scale(pieces[i][g], l, M);
+    sum = fmaf(a, l, sum);
+    if (scale) scale[i] = a;
   }
 #pragma unroll
-  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  for (int w = kLanes / 2; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
 }
 
 template <typename T, int D>
@@ -842,7 +836,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   constexpr int kRows = kJoinThreads / D;
   __shared__ float red[kRows][D];
   __shared__ float scale[kBlocks], total;
-  __shared__ float head_lse[kMaxG];
+  __shared__ float head_lse[kJoinThreads / 32][kMaxG];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_kv = cache.n_kv_heads;
   pdl_wait();
@@ -851,8 +845,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     const Run run = work.runs[c];
     if (run.seq < 0) return;
     const int blocks = blocks_for(run.units);
-    int64_t u = run_begin(c, run.units, blocks);
-    const int64_t run_hi = run_begin(c + 1, run.units, blocks);
+    // each warp takes an eighth of the run: a piece is a chain of dependent
+    // loads (counts, partial results, scores), and they then run side by side
+    constexpr int kParts = kJoinThreads / 32;
+    const int64_t run_lo = run_begin(c, run.units, blocks);
+    const int64_t run_units = run_begin(c + 1, run.units, blocks) - run_lo;
+    int64_t u = run_lo + warp * run_units / kParts;
+    const int64_t run_hi = run_lo + (warp + 1) * run_units / kParts;
     int64_t seq_first = run.seq_first;
     int b = run.seq;
     while (u < run_hi) {
@@ -874,22 +873,23 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       const int t_lo = int(u - first) * L::kUnit;
       const int t_hi = int(min(int64_t(n), (u_end - first) * L::kUnit));
       const Pieces pieces(work, G, D, first, head_units, run.units, blocks);
-      __syncthreads();
-      if (warp < G) {
+      const int64_t row0 = (int64_t(b) * n_kv + h) * G;
+      {  // four lanes per query head
+        const int g = min(lane / 4, G - 1);
         float x;
         if (pieces.n > 1) {
           float M, sum;
-          join_stats(pieces, G, warp, lane, M, sum, nullptr);
-          x = sum == 0.f ? INFINITY : M + log2f(sum);
+          join_stats<4>(pieces, G, g, lane % 4, M, sum, nullptr);
+          x = final_lse2(M, sum);
         } else {
-          x = lse[(int64_t(b) * n_kv + h) * G + warp] / kLn2;
-          if (x == -INFINITY) x = INFINITY;
+          x = lse[row0 + g] / kLn2;
         }
-        if (lane == 0) head_lse[warp] = x;
+        head_lse[warp][g] = x == -INFINITY ? INFINITY : x;
       }
-      __syncthreads();
+      __syncwarp();
       add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
-                        work.scores + first * L::kUnit * G, head_lse);
+                        work.scores + first * L::kUnit * G, head_lse[warp], lane, 32);
+      __syncwarp();
       u = u_end;
     }
   } else {
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
                         blocks_for(run.units));
     if (warp == 0) {
       float M, sum;
-      join_stats(pieces, G, g, lane, M, sum, scale);
+      join_stats<32>(pieces, G, g, lane, M, sum, scale);
       if (lane == 0) {
         total = sum;
         lse[row] = final_lse2(M, sum) * kLn2;
