@@ -1202,12 +1202,15 @@ PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumul
   const int unit = bf16 ? (d == 128 ? pdec::Tile<__nv_bfloat16, 128>::kUnit
                                     : pdec::Tile<__nv_bfloat16, 64>::kUnit)
                         : (d == 128 ? pdec::Tile<float, 128>::kUnit : pdec::Tile<float, 64>::kUnit);
-  const size_t slots = ((size_t(c->max_pages) * c->page_size + unit - 1) / unit +
-                        pdec::kHeadUnits) * unit;
+  const size_t head_units =
+      (size_t(c->max_pages) * c->page_size + unit - 1) / unit + pdec::kHeadUnits;
+  const size_t slots = head_units * unit;
   const size_t score_bytes =
       accumulate ? align256(slots * cfg->batch * cfg->n_q_heads * 4) : 0;
   char* p = static_cast<char*>(base);
   PagedWork w = {};
+  // the kernels count units in 32 bits
+  if (head_units * cfg->batch * cfg->n_kv_heads > 0x7fffffff) return w;
   w.bytes = runs_bytes + part_bytes + score_bytes;
   if (base) {
     w.work.runs = reinterpret_cast<pdec::Run*>(p);
@@ -1280,8 +1283,9 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
   for (const void* p : {q, static_cast<const void*>(n_slots), static_cast<const void*>(o),
                         static_cast<const void*>(lse), static_cast<const void*>(workspace)})
     if (!p || !aligned16(p)) return HGA_ERR_INVALID_ARG;
-  if (ws_bytes < hga_paged_decode_workspace_size(cfg, cache, accumulate))
-    return HGA_ERR_WORKSPACE;
+  const size_t need = hga_paged_decode_workspace_size(cfg, cache, accumulate);
+  if (need == 0) return HGA_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return HGA_ERR_WORKSPACE;
   const PagedView view = paged_view(cfg, cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const float scale_log2 = cfg->scale * 1.4426950408889634f;

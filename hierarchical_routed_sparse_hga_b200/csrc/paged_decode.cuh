@@ -75,14 +75,17 @@ struct Tile {
 
 // What a block of the decode kernel leaves for the join kernel: where its run
 // begins, and the head that begins in its last piece and goes on in the next
-// block's run (tail_units 0: none does)
+// block's run (tail_units 0: none does).  Units are counted in 32 bits: the
+// call refuses tables that could hold more.
 struct alignas(16) Run {
-  int64_t units;       // of the whole batch
-  int64_t seq_first;   // units before sequence `seq`
-  int64_t tail_first;  // units before the head
-  int32_t tail_units;  // units of the head
-  int32_t tail_head;   // sequence * n_kv_heads + head
+  int32_t units;       // of the whole batch
   int32_t seq;         // in which the run begins; -1: the block has no run
+  int32_t seq_first;   // units before it
+  int32_t tail_head;   // sequence * n_kv_heads + head
+  int32_t tail_first;  // units before the head
+  int32_t tail_units;  // units of the head
+  int32_t tail_part;   // slot of its first partial result
+  int32_t tail_n;      // number of its partial results
 };
 
 struct Work {
@@ -99,21 +102,28 @@ struct Work {
 // to 8190 slots take 186 us instead of 169.
 constexpr int kHeadUnits = 2;
 
-// blocks in use, the run of block c, and the block that holds unit u
-__host__ __device__ __forceinline__ int blocks_for(int64_t units) {
-  return int(units < kBlocks ? units : kBlocks);
-}
-__device__ __forceinline__ int64_t run_begin(int c, int64_t units, int blocks) {
-  return int64_t(c) * units / blocks;
-}
-__device__ __forceinline__ int block_of(int64_t u, int64_t units, int blocks) {
-  return int(((u + 1) * blocks - 1) / units);
-}
-// where block c puts the piece of a (sequence, head) that begins at unit u0:
-// its first piece is slot 0, its last slot 1
-__device__ __forceinline__ int part_slot(int c, int64_t u0, int64_t run_lo) {
-  return 2 * c + (u0 > run_lo ? 1 : 0);
-}
+// The runs of the blocks in use: q units each, the first r one more.
+struct Runs {
+  int blocks, q, r;
+  __device__ __forceinline__ explicit Runs(int units) {
+    blocks = min(units, kBlocks);
+    q = blocks > 0 ? units / blocks : 0;
+    r = units - q * blocks;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int block_of(int u) const {
+    const int wide = r * (q + 1);
+    return u < wide ? u / (q + 1) : r + (u - wide) / q;
+  }
+  // partial results of a head of `units` units from unit `first` on: the
+  // blocks' pieces of it; a block puts its first piece in slot 0 of its two,
+  // its last in slot 1 (only the head's first block can have it as its last)
+  __device__ __forceinline__ void pieces(int first, int units, int& part, int& n) const {
+    const int c0 = block_of(first);
+    n = block_of(first + units - 1) - c0 + 1;
+    part = 2 * c0 + (first > begin(c0) ? 1 : 0);
+  }
+};
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -528,14 +538,14 @@ struct Shared {
   Queries<T, D> q;
   float wo[kWarps][kMaxG][D];
   float wm[kWarps][kMaxG], wl[kWarps][kMaxG];
-  int64_t scan[kWarps];
+  int scan[kWarps];
   // the block's place in its run and the piece at hand: kept here rather than
   // in registers, which the tiles need
-  int64_t run_lo, u, run_hi;  // the run, and its next unit
-  int64_t seq_first;     // units before sequence `seq`
-  int64_t part;          // where the partial result goes; -1: the piece is whole
-  int64_t score;         // first score of the head
+  int run_lo, u, run_hi;  // the run, and its next unit
+  int seq_first;          // units before sequence `seq`
   int seq, head, t_lo, t_hi;
+  int part;               // slot of the partial result; -1: the piece is whole
+  int first;              // units before the head's slots
 };
 
 // grid kBlocks
@@ -552,34 +562,45 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   pdl_launch_dependents();
 
   // ---- the block's run of units -------------------------------------------
-  auto units_of = [&](int b) -> int64_t {
-    const int n = n_slots[b];
+  auto units_of = [&](int n) {
     return n > 0 && int64_t(n) <= cache.capacity()
-               ? int64_t(n_kv) * ((n + L::kUnit - 1) / L::kUnit + kHeadUnits)
+               ? n_kv * ((n + L::kUnit - 1) / L::kUnit + kHeadUnits)
                : 0;
   };
   const int per = (batch + kThreads - 1) / kThreads;
   const int b_lo = min(batch, tid * per), b_hi = min(batch, b_lo + per);
-  int64_t mine = 0;
+  int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    mine += units_of(b);
     const int n = n_slots[b];
+    mine += units_of(n);
     if (blockIdx.x == 0 && (n < 0 || int64_t(n) > cache.capacity()))
       latch_status(HGA_ERR_DEVICE_CHECK);
   }
-  int64_t incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, w);
+    const int x = __shfl_up_sync(0xffffffffu, incl, w);
     if (lane >= w) incl += x;
   }
   if (lane == 31) sh.scan[warp] = incl;
   __syncthreads();
-  int64_t before = incl - mine, units = 0;
+  int before = incl - mine, units = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sh.scan[w];
     units += sh.scan[w];
+  }
+  const Runs runs(units);
+  // the thread whose sequences hold the run's first unit finds it there
+  const int run_lo = runs.begin(blockIdx.x);
+  if (int(blockIdx.x) < runs.blocks && before <= run_lo && run_lo < before + mine) {
+    int at = before, b = b_lo;
+    for (int x; run_lo >= at + (x = units_of(n_slots[b])); ++b) at += x;
+    sh.run_lo = sh.u = run_lo;
+    sh.run_hi = runs.begin(blockIdx.x + 1);
+    sh.seq = b;
+    sh.seq_first = at;
+    work.runs[blockIdx.x] = {units, b, at, 0, 0, 0, 0, 0};
   }
   // idle sequences have no unit: nothing to attend to
   for (int b = blockIdx.x; b < batch; b += kBlocks) {
@@ -589,53 +610,43 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       o[row * D + i] = from_float<T>(0.f);
     for (int i = tid; i < n_kv * G; i += kThreads) lse[row + i] = -INFINITY;
   }
-  const int blocks = blocks_for(units);
-  if (int(blockIdx.x) >= blocks) {
-    if (tid == 0) work.runs[blockIdx.x] = {units, 0, 0, 0, 0, -1};
+  if (int(blockIdx.x) >= runs.blocks) {
+    if (tid == 0) work.runs[blockIdx.x] = {units, -1, 0, 0, 0, 0, 0, 0};
     return;
-  }
-  const int64_t run_lo = run_begin(blockIdx.x, units, blocks);
-  if (before <= run_lo && run_lo < before + mine) {  // one thread: its sequences hold run_lo
-    int64_t at = before;
-    int b = b_lo;
-    while (run_lo >= at + units_of(b)) at += units_of(b++);
-    sh.run_lo = sh.u = run_lo;
-    sh.run_hi = run_begin(blockIdx.x + 1, units, blocks);
-    sh.seq = b;
-    sh.seq_first = at;
-    work.runs[blockIdx.x] = {units, at, 0, 0, 0, b};
   }
 
   // ---- its pieces -----------------------------------------------------------
   while (true) {
     __syncthreads();  // also: the next piece overwrites the warps' results
     if (tid == 0 && sh.u < sh.run_hi) {
-      const int64_t u = sh.u;
-      int b = sh.seq;
-      int64_t seq_first = sh.seq_first, seq_units = units_of(b);
+      const int u = sh.u;
+      int b = sh.seq, seq_first = sh.seq_first, n = n_slots[b], seq_units = units_of(n);
       while (u >= seq_first + seq_units) {
         seq_first += seq_units;
-        seq_units = units_of(++b);
+        seq_units = units_of(n = n_slots[++b]);
       }
-      const int stride = int(seq_units / n_kv), h = int((u - seq_first) / stride);
-      const int64_t first = seq_first + int64_t(h) * stride + kHeadUnits;  // of the head's slots
-      const int64_t end = first + stride - kHeadUnits, u_end = min(sh.run_hi, end);
-      const int64_t u_lo = max(u, first);
+      const int stride = seq_units / n_kv, h = (u - seq_first) / stride;
+      const int first = seq_first + h * stride + kHeadUnits;  // of the head's slots
+      const int end = first + stride - kHeadUnits, u_end = min(sh.run_hi, end);
+      const int u_lo = max(u, first);
       const bool begins = u_lo == first, ends = u_end == end;
       if (begins && !ends && u_lo < u_end) {
         Run* run = work.runs + blockIdx.x;
+        run->tail_head = b * n_kv + h;
         run->tail_first = first;
         run->tail_units = stride - kHeadUnits;
-        run->tail_head = b * n_kv + h;
+        int part, n_parts;
+        Runs(units).pieces(first, stride - kHeadUnits, part, n_parts);
+        run->tail_part = part;
+        run->tail_n = n_parts;
       }
       sh.seq = b;
       sh.seq_first = seq_first;
       sh.head = h;
-      sh.t_lo = int(u_lo - first) * L::kUnit;
-      sh.t_hi = int(min(int64_t(n_slots[b]), (u_end - first) * L::kUnit));
-      sh.part = begins && ends ? -1
-                               : part_slot(blockIdx.x, first, sh.run_lo) * int64_t(G) * (D + 2);
-      sh.score = first * L::kUnit * G;
+      sh.t_lo = (u_lo - first) * L::kUnit;
+      sh.t_hi = min(n, (u_end - first) * L::kUnit);
+      sh.part = begins && ends ? -1 : 2 * int(blockIdx.x) + (first > sh.run_lo ? 1 : 0);
+      sh.first = first;
       sh.u = u_end;
     } else if (tid == 0) {
       sh.head = -1;
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const int b = sh.seq, h = sh.head;
       attend<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h,
                    q + (int64_t(b) * n_kv + h) * G * D, G, sh.t_lo, sh.t_hi, scale_log2,
-                   work.scores ? work.scores + sh.score : nullptr, sh.q, acc);
+                   work.scores ? work.scores + int64_t(sh.first) * L::kUnit * G : nullptr, sh.q, acc);
     }
     const int64_t row0 = (int64_t(sh.seq) * n_kv + sh.head) * G;
     merge_warps(acc, sh.wo, sh.wm, sh.wl, G, [&](int g, int e, float M, float sum, float out) {
@@ -656,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         o[(row0 + g) * D + e] = final_out<T>(out, sum);
         if (e == 0) lse[row0 + g] = final_lse2(M, sum) * kLn2;
       } else {
-        float* part = work.part + sh.part;
+        float* part = work.part + int64_t(sh.part) * G * (D + 2);
         part[2 * G + g * D + e] = out;
         if (e == 0) {
           part[g] = M;
@@ -784,22 +795,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// The pieces of a (sequence, head) that are joined: partial results first,
-// first + step, ...  Only the first block can have it as its last piece (see
-// part_slot), so one division finds them all.
+// The partial results of a (sequence, head): the first, then one in slot 0 of
+// each block that follows.
 struct Pieces {
   const float* first;
   const float* rest;  // of the second piece
-  int64_t step;
-  int n;
-  __device__ __forceinline__ Pieces(const Work& work, int G, int d, int64_t head_first,
-                                    int head_units, int64_t units, int blocks) {
-    const int c0 = block_of(head_first, units, blocks);
-    n = block_of(head_first + head_units - 1, units, blocks) - c0 + 1;
-    const int64_t size = int64_t(G) * (d + 2);
+  int step, n;
+  __device__ __forceinline__ Pieces(const Work& work, int G, int d, int part, int n) : n(n) {
+    const int size = G * (d + 2);
     step = 2 * size;
-    first = work.part + part_slot(c0, head_first, run_begin(c0, units, blocks)) * size;
-    rest = work.part + 2 * int64_t(c0 + 1) * size;
+    first = work.part + int64_t(part) * size;
+    rest = work.part + int64_t(part / 2 + 1) * step;
   }
   __device__ __forceinline__ const float* operator[](int i) const {
     return i == 0 ? first : rest + (i - 1) * step;
@@ -844,16 +850,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     const int c = int(blockIdx.x);
     const Run run = work.runs[c];
     if (run.seq < 0) return;
-    const int blocks = blocks_for(run.units);
+    const Runs runs(run.units);
     // each warp takes an eighth of the run: a piece is a chain of dependent
     // loads (counts, partial results, scores), and they then run side by side
     constexpr int kParts = kJoinThreads / 32;
-    const int64_t run_lo = run_begin(c, run.units, blocks);
-    const int64_t run_units = run_begin(c + 1, run.units, blocks) - run_lo;
-    int64_t u = run_lo + warp * run_units / kParts;
-    const int64_t run_hi = run_lo + (warp + 1) * run_units / kParts;
-    int64_t seq_first = run.seq_first;
-    int b = run.seq;
+    const int run_lo = runs.begin(c), run_units = runs.begin(c + 1) - run_lo;
+    int u = run_lo + int(int64_t(warp) * run_units / kParts);
+    const int run_hi = run_lo + int(int64_t(warp + 1) * run_units / kParts);
+    int seq_first = run.seq_first, b = run.seq;
     while (u < run_hi) {
       int n, stride;
       while (true) {
@@ -861,18 +865,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
         stride = n > 0 && int64_t(n) <= cache.capacity()
                      ? (n + L::kUnit - 1) / L::kUnit + kHeadUnits
                      : 0;
-        if (u < seq_first + int64_t(stride) * n_kv) break;
-        seq_first += int64_t(stride) * n_kv;
+        if (u < seq_first + stride * n_kv) break;
+        seq_first += stride * n_kv;
         ++b;
       }
-      const int h = int((u - seq_first) / stride), head_units = stride - kHeadUnits;
-      const int64_t first = seq_first + int64_t(h) * stride + kHeadUnits;
-      const int64_t u_end = min(run_hi, first + head_units);
+      const int h = (u - seq_first) / stride, head_units = stride - kHeadUnits;
+      const int first = seq_first + h * stride + kHeadUnits;
+      const int u_end = min(run_hi, first + head_units);
       u = max(u, first);
       if (u >= u_end) break;
-      const int t_lo = int(u - first) * L::kUnit;
-      const int t_hi = int(min(int64_t(n), (u_end - first) * L::kUnit));
-      const Pieces pieces(work, G, D, first, head_units, run.units, blocks);
+      const int t_lo = (u - first) * L::kUnit, t_hi = min(n, (u_end - first) * L::kUnit);
+      int part, n_parts;
+      runs.pieces(first, head_units, part, n_parts);
+      const Pieces pieces(work, G, D, part, n_parts);
       const int64_t row0 = (int64_t(b) * n_kv + h) * G;
       {  // four lanes per query head
         const int g = min(lane / 4, G - 1);
@@ -888,7 +893,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       }
       __syncwarp();
       add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
-                        work.scores + first * L::kUnit * G, head_lse[warp], lane, 32);
+                        work.scores + int64_t(first) * L::kUnit * G, head_lse[warp], lane,
+                        32);
       __syncwarp();
       u = u_end;
     }
@@ -897,8 +903,16 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     const Run run = work.runs[(int(blockIdx.x) - adders) % kBlocks];
     if (run.tail_units == 0) return;
     const int64_t row = int64_t(run.tail_head) * G + g;
-    const Pieces pieces(work, G, D, run.tail_first, run.tail_units, run.units,
-                        blocks_for(run.units));
+    const Pieces pieces(work, G, D, run.tail_part, run.tail_n);
+    // the outputs are on their way while the maxima and sums are
+    constexpr int kHeld = 8;
+    const int e = tid % D, r = tid / D;
+    float held[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = r + k * kRows;
+      held[k] = i < pieces.n ? pieces[i][2 * G + g * D + e] : 0.f;
+    }
     if (warp == 0) {
       float M, sum;
       join_stats<32>(pieces, G, g, lane, M, sum, scale);
@@ -908,10 +922,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       }
     }
     __syncthreads();
-    const int e = tid % D, r = tid / D;
     float out = 0.f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = r + k * kRows;
+      if (i < pieces.n) out = fmaf(scale[i], held[k], out);
+    }
 #pragma unroll 8
-    for (int i = r; i < pieces.n; i += kRows)
+    for (int i = r + kHeld * kRows; i < pieces.n; i += kRows)
       out = fmaf(scale[i], pieces[i][2 * G + g * D + e], out);
     red[r][e] = out;
     __syncthreads();

@@ -542,7 +542,9 @@ HGA_API hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_pages_t
                                       const int64_t* pos, float rope_base, void* q_out,
                                       void* stream);
 
-/* Bytes of device workspace hga_paged_decode needs (0 for bad arguments). */
+/* Bytes of device workspace hga_paged_decode needs (0 for bad arguments, and
+ * where batch * n_kv_heads * max_pages * page_size reaches 2^36 slots or so,
+ * which the call refuses with HGA_ERR_UNSUPPORTED). */
 HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hga_pages_t* cache,
                                                int32_t accumulate);
 

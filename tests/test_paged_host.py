@@ -136,6 +136,12 @@ def test_decode_refusals():
         assert decode(c, p, acc=acc, size=need - 1) == 6
 
 
+def test_decode_refuses_tables_whose_units_pass_32_bits():
+    c, p = cfg(batch=1024), pages(max_pages=1 << 20)
+    assert hga.hga_paged_decode_workspace_size(c, p, False) == 0
+    assert decode(c, p) == 2
+
+
 def test_append_refusals():
     c, p = cfg(), pages()
     for kw in (dict(k=0), dict(v=0), dict(n=0), dict(pos=0), dict(q=0), dict(q_out=0),
