@@ -304,6 +304,11 @@ KERNEL_SOURCE = {
     "attn_bwd_dq_simt": ("attn_simt.cuh",), "attn_bwd_dkdv_simt": ("attn_simt.cuh",),
     "tier_dedup": ("tier.cuh",), "tier_copy": ("tier.cuh",),
     "decode": ("decode.cuh", "route.cuh"), "prepare": ("prepare.cuh",),
+    "paged_append": ("paged.cuh", "paged_append.cuh"),
+    "paged_decode": ("paged.cuh", "paged_decode.cuh"),
+    "paged_join": ("paged.cuh", "paged_decode.cuh"),
+    "paged_evict": ("paged.cuh", "paged_evict.cuh"),
+    "paged_move": ("paged.cuh", "paged_evict.cuh"),
 }
 SHARED_SOURCES = ("hga_common.cuh", "sm100_ptx.cuh")
 

@@ -1231,7 +1231,8 @@ extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_page
                                          void* stream) {
   hga_status_t st = check_pages(cfg, cache);
   if (st != HGA_OK) return st;
-  if (!k_proj || !v_proj || !n_slots || !pos || (q_proj == nullptr) != (q_out == nullptr))
+  if (!k_proj || !v_proj || !n_slots || !pos || (q_proj == nullptr) != (q_out == nullptr) ||
+      (q_out && q_out == q_proj))
     return HGA_ERR_INVALID_ARG;
   for (const void* p : {q_proj, k_proj, v_proj, static_cast<const void*>(n_new),
                         static_cast<const void*>(n_slots), static_cast<const void*>(pos),
@@ -1283,6 +1284,11 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
   for (const void* p : {q, static_cast<const void*>(n_slots), static_cast<const void*>(o),
                         static_cast<const void*>(lse), static_cast<const void*>(workspace)})
     if (!p || !aligned16(p)) return HGA_ERR_INVALID_ARG;
+  // blocks write a head's output while others read the queries
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t q_bytes = uintptr_t(cfg->batch) * cfg->n_q_heads * cfg->head_dim *
+                            (cfg->dtype == HGA_BF16 ? 2 : 4);
+  if (qa < oa + q_bytes && oa < qa + q_bytes) return HGA_ERR_INVALID_ARG;
   const size_t need = hga_paged_decode_workspace_size(cfg, cache, accumulate);
   if (need == 0) return HGA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return HGA_ERR_WORKSPACE;

@@ -18,14 +18,19 @@ kernel reads HBM, so DRAM counters keep their meaning.
   tier      host tier, batch 8 x 8192 tokens, 4 segments fwd+bwd
   simt      the CUDA-core kernels: float32, d = 64, 4 query heads / 1 KV
             head, batch 2, 4 segments of 1024 after 4096 history tokens
+  paged     the paged cache, batch 4, pages of 64: prompts of 16384 tokens
+            appended, three decode steps with accumulated weights, the cache
+            cut to 8192 slots
 """
 import sys
 
 import torch
 
-from . import HGA_BF16, HGA_F32, Config, HgaLayer, HgaTieredLayer, hga_build_summaries, synth
+from . import (HGA_BF16, HGA_F32, Config, HgaLayer, HgaPagedLayer, HgaTieredLayer,
+               hga_build_summaries, synth)
 
 CASES = ("bench16k", "long128k", "decode", "prepare", "tier", "simt")
+SERVING_CASES = ("paged",)
 
 
 def _qwen3(batch, ctx, **kw):
@@ -99,8 +104,30 @@ def run(case, dev):
         hga_build_summaries(layer.cfg, layer.k, w.ctx_len, 0, 4096, layer.gsum, layer.bsum)
         for i, s0 in enumerate(w.segments()):
             layer.segment(qs[i], s0, dos[i])
+    elif case == "paged":
+        B, Hq, Hkv, d, T = 4, 32, 8, 128, 16384
+        layer = HgaPagedLayer(Config(B, Hq, Hkv, d, 1, 1, HGA_BF16), B * T // 64 + B, 64,
+                              T // 64 + 1, device=dev)
+        g = torch.Generator(device=dev)
+        g.manual_seed(63)
+        layer.table.copy_(torch.randperm(layer.table.numel(), generator=g,
+                                         device=dev).view(B, -1).to(torch.int32))
+
+        def append(n, q_out):
+            qkv = torch.randn((B, n, (Hq + 2 * Hkv) * d), generator=g, device=dev).to(torch.bfloat16)
+            layer.advance(n)
+            layer.append(*qkv.split([Hq * d, Hkv * d, Hkv * d], -1), 1e6, q_out)
+
+        append(T - 8, torch.empty((B, Hq, T - 8, d), dtype=torch.bfloat16, device=dev))
+        q = torch.empty((B, Hq, 1, d), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((B, Hq), device=dev)
+        for _ in range(3):
+            append(1, q)
+            layer.decode(q.view(B, Hq, d), o, lse, accumulate=True)
+        layer.evict(8192, sinks=4, recent=64)
     else:
-        raise SystemExit(f"unknown case {case!r}; one of {', '.join(CASES)}")
+        raise SystemExit(f"unknown case {case!r}; one of {', '.join(CASES + SERVING_CASES)}")
     torch.cuda.synchronize(dev)
 
 
@@ -108,7 +135,7 @@ def main(argv=None):
     argv = sys.argv[1:] if argv is None else argv
     if len(argv) != 1:
         raise SystemExit(f"usage: python -m hierarchical_routed_sparse_hga_b200.profile_cases "
-                         f"<{'|'.join(CASES)}>")
+                         f"<{'|'.join(CASES + SERVING_CASES)}>")
     run(argv[0], torch.device("cuda", 0))
     print("ok", argv[0])
 

@@ -495,9 +495,9 @@ HGA_API hga_status_t hga_tier_write_segment(const hga_config_t* cfg, int fd_k, i
  * its last token: a step advances both, then calls hga_paged_append and
  * hga_paged_decode of every layer.  A sequence with n_slots = 0 is idle.
  *
- * Two sequences may share pages that they only read or decode from.  Pages
- * that hga_paged_append writes or hga_paged_evict cuts belong to one sequence
- * of the call.
+ * Two sequences may share pages that they only decode from.  Pages that
+ * hga_paged_append writes or hga_paged_evict cuts belong to one sequence of
+ * the call and stand once in its table.
  *
  * cfg->topk_blocks and cfg->topk_groups are not used by these calls.  Device
  * checks: a count outside [0, max_pages*page_size] leaves the sequence's
@@ -527,7 +527,8 @@ typedef struct {
  * n_slots[b] - n_new[b] + i and has position pos[b] - n_new[b] + 1 + i, which
  * must lie in [0, 2^31).  Q and K are rotated as in hga_prepare_segment
  * (rope_base 0 or 1: not rotated), V is not.  q_out [batch, n_q_heads, s_new,
- * head_dim] receives Q; q_proj and q_out may both be NULL (K and V only).
+ * head_dim] receives Q (not in place); q_proj and q_out may both be NULL (K and
+ * V only).
  * Where the records are kept, a new slot's weight becomes 0 and its slot_pos
  * its position.  Rows i >= n_new[b] of q_out are left as they were.  A
  * sequence whose counts or positions are out of range is left out, and a
@@ -552,7 +553,7 @@ HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hg
  * Attention of one new token per sequence over all its n_slots[b] slots:
  *   s_j = scale q.k_j;  O = softmax(s) V;  LSE = log(sum_j exp(s_j))
  * for each of the G heads of every KV head.  q, o [batch, n_q_heads,
- * head_dim] (cfg->dtype), lse [batch, n_q_heads] float32.  accumulate = 1
+ * head_dim] (cfg->dtype, not overlapping), lse [batch, n_q_heads] float32.  accumulate = 1
  * adds the softmax weight of every slot, summed over the G heads, to
  * cache->weight (which must then not be NULL):
  *   weight[slot] += sum_g exp(s_gj - LSE_g).

@@ -81,12 +81,12 @@ def status_of(fn, *args):
     return e.value.status
 
 
-def decode(c, p, q=FAKE, n=FAKE, acc=0, o=FAKE, lse=FAKE, ws=FAKE, size=1 << 40):
+def decode(c, p, q=FAKE, n=FAKE, acc=0, o=FAKE << 8, lse=FAKE, ws=FAKE, size=1 << 40):
     return status_of(hga.hga_paged_decode, c, p, q, n, acc, o, lse, ws, size, 0)
 
 
 def append(c, p, q=FAKE, k=FAKE, v=FAKE, qs=32 * 128, kvs=8 * 128, s_new=1, n_new=FAKE, n=FAKE,
-           pos=FAKE, base=1e6, q_out=FAKE):
+           pos=FAKE, base=1e6, q_out=FAKE << 8):
     return status_of(hga.hga_paged_append, c, p, q, k, v, qs, kvs, s_new, n_new, n, pos, base,
                      q_out, 0)
 
@@ -127,7 +127,7 @@ def test_every_call_checks_the_config(kw, status):
 def test_decode_refusals():
     c, p = cfg(), pages()
     for kw in (dict(q=0), dict(n=0), dict(o=0), dict(lse=0), dict(ws=0), dict(o=FAKE + 8),
-               dict(acc=2)):
+               dict(o=FAKE), dict(o=FAKE + 2 * 32 * 128 * 2 - 16), dict(acc=2)):
         assert decode(c, p, **kw) == 1, kw
     assert decode(c, pages(weight=None), acc=1) == 1
     for acc in (0, 1):
@@ -145,7 +145,7 @@ def test_decode_refuses_tables_whose_units_pass_32_bits():
 def test_append_refusals():
     c, p = cfg(), pages()
     for kw in (dict(k=0), dict(v=0), dict(n=0), dict(pos=0), dict(q=0), dict(q_out=0),
-               dict(q=FAKE + 2), dict(s_new=-1), dict(base=-1.0), dict(base=float("nan")),
+               dict(q=FAKE + 2), dict(q_out=FAKE), dict(s_new=-1), dict(base=-1.0), dict(base=float("nan")),
                dict(qs=32 * 128 - 8), dict(kvs=8 * 128 - 8), dict(qs=32 * 128 + 4),
                dict(kvs=8 * 128 + 4), dict(kvs=1 << 33)):
         assert append(c, p, **kw) == 1, kw
