@@ -92,6 +92,8 @@ class PagedCache:
 
     def __init__(self, cfg: Config, k, v, table, weight=None, slot_pos=None):
         import torch
+        self.torch, self.int32, self.int64, self.float32 = (torch, torch.int32, torch.int64,
+                                                            torch.float32)
         dt = torch.bfloat16 if cfg.dtype == HGA_BF16 else torch.float32
         if k.dim() != 4:
             raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim]")
@@ -135,6 +137,7 @@ class PagedCache:
             slot_pos=None):
         """The same over raw device addresses of the current device."""
         self = cls.__new__(cls)
+        self.int32 = self.int64 = self.float32 = None  # the types of raw calls' tensors
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
         self.device = self.index = self.dtype = self.batch = None
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
@@ -483,11 +486,7 @@ def hga_segment_fwd_bwd(cfg: Config, q, k, v, ctx_cap, q_begin, s_len, bsum, gsu
 # paged key-value cache
 # ----------------------------------------------------------------------------
 
-def _paged_arg(cache: PagedCache, name, x, dtype, numel):
-    """Device address of a call's tensor (or raw address), checked against the
-    cache's device and the type and size the call reads or writes."""
-    if x is None or isinstance(x, int):
-        return x
+def _paged_refuse(cache: PagedCache, name, x, dtype, numel):
     if not x.is_cuda:
         raise ValueError("libhga takes device tensors")
     if cache.index is not None and x.get_device() != cache.index:
@@ -498,6 +497,16 @@ def _paged_arg(cache: PagedCache, name, x, dtype, numel):
         raise ValueError("libhga takes contiguous tensors")
     if x.numel() < numel:
         raise ValueError(f"{name} must hold {numel} elements")
+
+
+def _paged_arg(cache: PagedCache, name, x, dtype, numel):
+    """Device address of a call's tensor (or raw address), checked against the
+    cache's device and the type and size the call reads or writes."""
+    if x is None or isinstance(x, int):
+        return x
+    if (x.get_device() != cache.index or x.dtype is not dtype or x.numel() < numel
+            or not x.is_contiguous()):
+        _paged_refuse(cache, name, x, dtype, numel)
     return x.data_ptr()
 
 
@@ -506,12 +515,12 @@ def _paged_call(name, fn, cache: PagedCache, cfg: _Config, stream, *args):
     if cache.batch is not None and cache.batch != cfg.batch:
         raise ValueError("the cache was described for another batch")
     if cache.index is not None:
-        import torch
-        if cache.index != torch.cuda.current_device():
-            with torch.cuda.device(cache.index):
+        cuda = cache.torch.cuda
+        if cache.index != cuda.current_device():
+            with cuda.device(cache.index):
                 return _check(name, fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream)))
         if stream is None:  # the address alone: a stream object costs 3 us
-            stream = torch._C._cuda_getCurrentRawStream(cache.index)
+            stream = cache.torch._C._cuda_getCurrentRawStream(cache.index)
     status = fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream))
     if status != HGA_OK:
         _check(name, status)
@@ -521,7 +530,6 @@ def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_r
                      kv_row_stride, s_new, n_new, n_slots, pos, rope_base, q_out, stream=None):
     """New tokens into the cache, from their projection outputs (contiguous
     tensors, or raw addresses: three of one buffer for a fused QKV row)."""
-    import torch
     dt, B = cache.dtype, cfg.batch
     rows, d = max(B * s_new, 1) - 1, cfg.head_dim
     q_numel = rows * q_row_stride + cfg.n_q_heads * d
@@ -531,9 +539,9 @@ def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_r
                 _paged_arg(cache, "k_proj", k_proj, dt, kv_numel),
                 _paged_arg(cache, "v_proj", v_proj, dt, kv_numel),
                 q_row_stride, kv_row_stride, s_new,
-                _paged_arg(cache, "n_new", n_new, torch.int32, B),
-                _paged_arg(cache, "n_slots", n_slots, torch.int32, B),
-                _paged_arg(cache, "pos", pos, torch.int64, B), float(rope_base or 0.0),
+                _paged_arg(cache, "n_new", n_new, cache.int32, B),
+                _paged_arg(cache, "n_slots", n_slots, cache.int32, B),
+                _paged_arg(cache, "pos", pos, cache.int64, B), float(rope_base or 0.0),
                 _paged_arg(cache, "q_out", q_out, dt, B * cfg.n_q_heads * s_new * cfg.head_dim))
 
 
@@ -546,15 +554,14 @@ def hga_paged_decode(cfg: Config, cache: PagedCache, q, n_slots, accumulate, o, 
                      ws_bytes=None, stream=None):
     """One new token per sequence over all its slots; accumulate adds every
     slot's attention weight to cache.weight."""
-    import torch
     dt, rows = cache.dtype, cfg.batch * cfg.n_q_heads
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
     _paged_call("hga_paged_decode", load().hga_paged_decode, cache, cfg.c(), stream,
                 _paged_arg(cache, "q", q, dt, rows * cfg.head_dim),
-                _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch), int(accumulate),
+                _paged_arg(cache, "n_slots", n_slots, cache.int32, cfg.batch), int(accumulate),
                 _paged_arg(cache, "o", o, dt, rows * cfg.head_dim),
-                _paged_arg(cache, "lse", lse, torch.float32, rows),
-                _paged_arg(cache, "workspace", workspace, None, 0), ws_bytes)
+                _paged_arg(cache, "lse", lse, cache.float32, rows),
+                _paged_arg(cache, "workspace", workspace, getattr(workspace, "dtype", None), 0), ws_bytes)
 
 
 def hga_paged_evict_workspace_size(cfg: Config, cache: PagedCache) -> int:
@@ -565,12 +572,11 @@ def hga_paged_evict(cfg: Config, cache: PagedCache, n_slots, pos, keep, sinks, r
                     ws_bytes=None, stream=None):
     """Cuts every sequence to `keep` slots per KV head by accumulated weight
     (n_slots itself is the caller's to clamp)."""
-    import torch
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
     _paged_call("hga_paged_evict", load().hga_paged_evict, cache, cfg.c(), stream,
-                _paged_arg(cache, "n_slots", n_slots, torch.int32, cfg.batch),
-                _paged_arg(cache, "pos", pos, torch.int64, cfg.batch), keep, sinks, recent,
-                _paged_arg(cache, "workspace", workspace, None, 0), ws_bytes)
+                _paged_arg(cache, "n_slots", n_slots, cache.int32, cfg.batch),
+                _paged_arg(cache, "pos", pos, cache.int64, cfg.batch), keep, sinks, recent,
+                _paged_arg(cache, "workspace", workspace, getattr(workspace, "dtype", None), 0), ws_bytes)
 
 
 def hga_get_device_status(stream=None) -> int:
