@@ -125,7 +125,7 @@ class PagedCache:
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
         self.device, self.index, self.dtype = k.device, k.get_device(), dt
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, table.shape[1]
-        self.batch = cfg.batch
+        self.shape = (cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.dtype)
         stride = k.stride(0) if n_pages > 1 else heads * page_size * d
         self._c = _Pages(k.data_ptr(), v.data_ptr(), weight.data_ptr() if weight is not None else None,
                          slot_pos.data_ptr() if slot_pos is not None else None, table.data_ptr(),
@@ -139,7 +139,7 @@ class PagedCache:
         self = cls.__new__(cls)
         self.int32 = self.int64 = self.float32 = None  # the types of raw calls' tensors
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
-        self.device = self.index = self.dtype = self.batch = None
+        self.device = self.index = self.dtype = self.shape = None
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self._c = _Pages(k, v, weight, slot_pos, table, n_pages, page_stride, page_size, max_pages)
         self._ref = ctypes.byref(self._c)
@@ -512,9 +512,9 @@ def _paged_arg(cache: PagedCache, name, x, dtype, numel):
 
 def _paged_call(name, fn, cache: PagedCache, cfg: _Config, stream, *args):
     """Calls fn on the cache's device, on `stream` or that device's current one."""
-    if cache.batch is not None and cache.batch != cfg.batch:
-        raise ValueError("the cache was described for another batch")
     if cache.index is not None:
+        if cache.shape != (cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.dtype):
+            raise ValueError("the cache was described for another configuration")
         cuda = cache.torch.cuda
         if cache.index != cuda.current_device():
             with cuda.device(cache.index):

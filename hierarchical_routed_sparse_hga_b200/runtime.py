@@ -400,6 +400,8 @@ class HgaPagedLayer:
                                   or x.dtype != _TORCH_DTYPE[cfg.dtype]
                                   or x.shape[:2] != k_proj.shape[:2] or x.shape[0] != cfg.batch):
                 raise ValueError(f"{name}: type, device, batch or token count differ")
+        if k_proj.shape[1] == 0:
+            return
         kv_row = self._rows(k_proj, cfg.n_kv_heads, d, "k_proj")
         if self._rows(v_proj, cfg.n_kv_heads, d, "v_proj") != kv_row:
             raise ValueError("k_proj and v_proj must have the same row stride")

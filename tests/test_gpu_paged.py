@@ -264,6 +264,15 @@ def test_decode_sequences_that_share_pages():
     c.check_decode(before)
 
 
+def test_decode_a_page_that_stands_twice_in_the_table():
+    # its slots count twice, and their weights receive both shares
+    c = Case(lens=(100,), ps=16)
+    c.table[0, 5] = c.table[0, 1]
+    before = c.host()[2]
+    c.decode(True)
+    c.check_decode(before)
+
+
 def test_decode_captured_and_replayed_as_the_cache_grows():
     import torch
     c = Case(lens=(300, 2, 0, 64), ps=16)
@@ -358,6 +367,13 @@ def test_offsets_past_32_bits():
     hga.hga_paged_evict(c.cfg, c.cache, c.n_slots, c.pos, 20, 2, 4, c.workspace())
     assert (to_f64(k[at]) == kh[at.numpy()])[~np.isnan(kh[at.numpy()])].all()
     assert (to_f64(v[at]) == vh[at.numpy()])[~np.isnan(vh[at.numpy()])].all()
+    # the last token again, from new projections
+    kv = torch.randn((2, 2, 1, 2, 128), device="cuda").to(torch.bfloat16)
+    hga.hga_paged_append(c.cfg, c.cache, None, kv[0], kv[1], 0, 256, 1, None, c.n_slots, c.pos, 0.0,
+                         None)
+    for b, n in enumerate(c.lens):
+        pg, row = int(c.table[b, (n - 1) // 16]), (n - 1) % 16
+        assert torch.equal(k[pg, :, row], kv[0, b, 0]) and torch.equal(v[pg, :, row], kv[1, b, 0])
     assert status() == 0
 
 
@@ -559,6 +575,17 @@ def test_evict_ties_zeros_and_values_that_are_no_numbers(n, keep):
     check_evict(c, keep, 4, 32)
 
 
+@pytest.mark.parametrize("levels", [0, 50])
+def test_evict_a_head_longer_than_the_blocks_hold(levels):
+    # more slots a block than its shared memory holds keys, and than one round
+    # of ranks covers; with 50 different weights the edge is a long tie
+    c = Case(lens=(540001,), Hkv=1, G=1, d=64, ps=256, spare=0)
+    if levels:
+        c.weight.copy_((c.weight * levels).floor())
+    check_evict(c, 270007, 4, 1000)
+    assert status() == 0
+
+
 def test_evict_positions_that_hold_more_than_is_kept():
     # repeated positions hold more slots than `keep`: the lower ones are kept
     c = Case(lens=(500,), ps=16)
@@ -685,6 +712,31 @@ def test_generation_with_a_bounded_cache(dtype):
     assert p_held is held
 
 
+def test_queries_of_the_append_feed_the_next_call():
+    """Back to back on one stream: the mean queries are read from what the
+    append wrote, not from what the buffer held."""
+    import torch
+    from hierarchical_routed_sparse_hga_b200 import (HGA_BF16, Config, HgaPagedLayer,
+                                                     hga_build_query_summaries)
+    B, Hkv, G, d, S = 2, 8, 4, 128, 2048
+    cfg = Config(B, Hkv * G, Hkv, d, 4, 16, HGA_BF16)
+    layer = HgaPagedLayer(cfg, B * S // 64, 64, S // 64)
+    layer.advance(S)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    qsum = torch.zeros((B, Hkv, S // 64, d), device="cuda")
+    for _ in range(5):
+        qkv = torch.randn((B, S, (Hkv * G + 2 * Hkv) * d), generator=g, device="cuda").to(torch.bfloat16)
+        q_out = torch.full((B, Hkv * G, S, d), math.nan, dtype=torch.bfloat16, device="cuda")
+        layer.append(*qkv.split([Hkv * G * d, Hkv * d, Hkv * d], -1), 1e6, q_out)
+        hga_build_query_summaries(cfg, q_out, 0, S, S, qsum)
+        want = q_out.view(B, Hkv, G, S // 64, 64, d).double().mean((2, 4))
+        # float32 sums of 256 values of size up to 6
+        assert float((qsum.double() - want).abs().max()) <= 256 * 6 * 2.0 ** -23
+    # nothing to append is no call
+    layer.append(qkv[:, :0, :4096], qkv[:, :0, :1024], qkv[:, :0, :1024], 1e6, q_out)
+
+
 def test_paged_and_routed_decode_agree_when_everything_is_selected():
     """The routed decode over a contiguous cache whose top-k covers it, and the
     paged decode over the same tokens."""
@@ -731,6 +783,10 @@ def test_binding_refuses_other_devices_types_and_sizes():
             hga.hga_paged_decode(*args)
     with pytest.raises(ValueError):
         hga.hga_paged_evict(c.cfg, c.cache, c.n_slots, c.pos.int(), 8, 0, 0, ws)
+    for other in (hga.Config(2, 8, 2, 64, 1, 1), hga.Config(2, 8, 4, 128, 1, 1),
+                  hga.Config(2, 8, 2, 128, 1, 1, hga.HGA_F32)):
+        with pytest.raises(ValueError):
+            hga.hga_paged_decode(other, *ok[1:])
     with pytest.raises(ValueError):
         cfg3 = hga.Config(3, 8, 2, 128, 1, 1)
         hga.hga_paged_evict(cfg3, c.cache, torch.zeros(3, dtype=torch.int32, device="cuda"),
