@@ -124,6 +124,7 @@ class PagedCache:
                 raise ValueError("a paged cache takes tensors of one CUDA device")
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
         self.device, self.index, self.dtype = k.device, k.get_device(), dt
+        self._kept = None
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, table.shape[1]
         self.shape = (cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.dtype)
         stride = k.stride(0) if n_pages > 1 else heads * page_size * d
@@ -139,7 +140,7 @@ class PagedCache:
         self = cls.__new__(cls)
         self.int32 = self.int64 = self.float32 = None  # the types of raw calls' tensors
         self.k, self.v, self.table, self.weight, self.slot_pos = k, v, table, weight, slot_pos
-        self.device = self.index = self.dtype = self.shape = None
+        self.device = self.index = self.dtype = self.shape = self._kept = None
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self._c = _Pages(k, v, weight, slot_pos, table, n_pages, page_stride, page_size, max_pages)
         self._ref = ctypes.byref(self._c)
@@ -502,26 +503,39 @@ def _paged_refuse(cache: PagedCache, name, x, dtype, numel):
 def _paged_arg(cache: PagedCache, name, x, dtype, numel):
     """Device address of a call's tensor (or raw address), checked against the
     cache's device and the type and size the call reads or writes."""
-    if x is None or isinstance(x, int):
+    try:
+        if (x.get_device() == cache.index and x.dtype is dtype and x.numel() >= numel
+                and x.is_contiguous()):
+            return x.data_ptr()
+    except AttributeError:  # an address, or None
         return x
-    if (x.get_device() != cache.index or x.dtype is not dtype or x.numel() < numel
-            or not x.is_contiguous()):
-        _paged_refuse(cache, name, x, dtype, numel)
+    _paged_refuse(cache, name, x, dtype, numel)
     return x.data_ptr()
 
 
-def _paged_call(name, fn, cache: PagedCache, cfg: _Config, stream, *args):
+def _paged_cfg(cache: PagedCache, cfg: Config):
+    """The C form of cfg, kept with the cache as long as cfg says the same."""
+    kept = cache._kept
+    if kept is not None and kept[0] == cfg.__dict__:
+        return kept[1]
+    if cache.shape is not None and cache.shape != (cfg.batch, cfg.n_kv_heads, cfg.head_dim,
+                                                   cfg.dtype):
+        raise ValueError("the cache was described for another configuration")
+    cache._kept = (dict(cfg.__dict__), ctypes.byref(cfg.c()))
+    return cache._kept[1]
+
+
+def _paged_call(name, fn, cache: PagedCache, cfg: Config, stream, *args):
     """Calls fn on the cache's device, on `stream` or that device's current one."""
+    ref = _paged_cfg(cache, cfg)
     if cache.index is not None:
-        if cache.shape != (cfg.batch, cfg.n_kv_heads, cfg.head_dim, cfg.dtype):
-            raise ValueError("the cache was described for another configuration")
         cuda = cache.torch.cuda
         if cache.index != cuda.current_device():
             with cuda.device(cache.index):
-                return _check(name, fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream)))
+                return _check(name, fn(ref, cache._ref, *args, _stream(stream)))
         if stream is None:  # the address alone: a stream object costs 3 us
             stream = cache.torch._C._cuda_getCurrentRawStream(cache.index)
-    status = fn(ctypes.byref(cfg), cache._ref, *args, _stream(stream))
+    status = fn(ref, cache._ref, *args, _stream(stream))
     if status != HGA_OK:
         _check(name, status)
 
@@ -534,7 +548,7 @@ def hga_paged_append(cfg: Config, cache: PagedCache, q_proj, k_proj, v_proj, q_r
     rows, d = max(B * s_new, 1) - 1, cfg.head_dim
     q_numel = rows * q_row_stride + cfg.n_q_heads * d
     kv_numel = rows * kv_row_stride + cfg.n_kv_heads * d
-    _paged_call("hga_paged_append", load().hga_paged_append, cache, cfg.c(), stream,
+    _paged_call("hga_paged_append", load().hga_paged_append, cache, cfg, stream,
                 _paged_arg(cache, "q_proj", q_proj, dt, q_numel),
                 _paged_arg(cache, "k_proj", k_proj, dt, kv_numel),
                 _paged_arg(cache, "v_proj", v_proj, dt, kv_numel),
@@ -556,7 +570,7 @@ def hga_paged_decode(cfg: Config, cache: PagedCache, q, n_slots, accumulate, o, 
     slot's attention weight to cache.weight."""
     dt, rows = cache.dtype, cfg.batch * cfg.n_q_heads
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _paged_call("hga_paged_decode", load().hga_paged_decode, cache, cfg.c(), stream,
+    _paged_call("hga_paged_decode", load().hga_paged_decode, cache, cfg, stream,
                 _paged_arg(cache, "q", q, dt, rows * cfg.head_dim),
                 _paged_arg(cache, "n_slots", n_slots, cache.int32, cfg.batch), int(accumulate),
                 _paged_arg(cache, "o", o, dt, rows * cfg.head_dim),
@@ -573,7 +587,7 @@ def hga_paged_evict(cfg: Config, cache: PagedCache, n_slots, pos, keep, sinks, r
     """Cuts every sequence to `keep` slots per KV head by accumulated weight
     (n_slots itself is the caller's to clamp)."""
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _paged_call("hga_paged_evict", load().hga_paged_evict, cache, cfg.c(), stream,
+    _paged_call("hga_paged_evict", load().hga_paged_evict, cache, cfg, stream,
                 _paged_arg(cache, "n_slots", n_slots, cache.int32, cfg.batch),
                 _paged_arg(cache, "pos", pos, cache.int64, cfg.batch), keep, sinks, recent,
                 _paged_arg(cache, "workspace", workspace, getattr(workspace, "dtype", None), 0), ws_bytes)
