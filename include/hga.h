@@ -527,12 +527,11 @@ typedef struct {
  * n_slots[b] - n_new[b] + i and has position pos[b] - n_new[b] + 1 + i, which
  * must lie in [0, 2^31).  Q and K are rotated as in hga_prepare_segment
  * (rope_base 0 or 1: not rotated), V is not.  q_out [batch, n_q_heads, s_new,
- * head_dim] receives Q (not in place); q_proj and q_out may both be NULL (K and
- * V only).
- * Where the records are kept, a new slot's weight becomes 0 and its slot_pos
- * its position.  Rows i >= n_new[b] of q_out are left as they were.  A
- * sequence whose counts or positions are out of range is left out, and a
- * token whose page is out of range is not stored (its Q is); both latch
+ * head_dim] receives Q (not in place); q_proj and q_out may both be NULL (K
+ * and V only).  Where the records are kept, a new slot's weight becomes 0 and
+ * its slot_pos its position.  Rows i >= n_new[b] of q_out are left as they
+ * were.  A sequence whose counts or positions are out of range is left out,
+ * and a token whose page is out of range is not stored (its Q is); both latch
  * HGA_ERR_DEVICE_CHECK.  One launch; no workspace.
  */
 HGA_API hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_pages_t* cache,
@@ -563,7 +562,10 @@ HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hg
  * finite (others make their head's results NaN or undefined numbers).  Deterministic (with accumulate = 1 as long
  * as no two sequences share a page).  workspace: at least
  * hga_paged_decode_workspace_size() bytes of device memory, 16-byte aligned,
- * whose contents do not matter; not used by two calls at once.
+ * whose contents do not matter; not used by two calls at once.  The counts
+ * are read on the device, so a captured call follows them.  One launch where
+ * the table is narrow enough for one thread-block cluster per (sequence, KV
+ * head), two otherwise.
  */
 HGA_API hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_pages_t* cache,
                                       const void* q, const int32_t* n_slots, int32_t accumulate,
@@ -589,7 +591,7 @@ HGA_API size_t hga_paged_evict_workspace_size(const hga_config_t* cfg, const hga
  * sinks + recent <= keep.  A sequence with more than `keep` slots that has a
  * page out of range among them is left untouched (HGA_ERR_DEVICE_CHECK is
  * latched).  workspace as above: at least hga_paged_evict_workspace_size()
- * bytes.
+ * bytes.  Two launches.
  */
 HGA_API hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
                                      const int32_t* n_slots, const int64_t* pos, int32_t keep,
