@@ -2,6 +2,7 @@
 
     from hierarchical_routed_sparse_hga_b200 import Config, HgaLayer
     from hierarchical_routed_sparse_hga_b200 import hga_route, hga_attn_fwd, ...
+    from hierarchical_routed_sparse_hga_b200 import HgaPagedLayer, PagedCache, hga_paged_decode
 
 The shared library is loaded on first use; build it with
 `python -m hierarchical_routed_sparse_hga_b200.build`.

@@ -7,10 +7,11 @@
 // Warps work on their own, without block barriers: the chain in front of a
 // token's rows (counts, page, angles) takes longer than the rows themselves,
 // so what counts is that many tokens are at different points of it: two rows
-// per lane in flight and 64 registers, not four and 80 (4 x 8192 tokens, ragged:
-// 91 us, 5.5 TB/s; 105 us), in blocks of four warps (of eight: 96 us).  A prompt
-// takes one warp per token, a decode step kTokenWarps (each then makes the
-// token's table of angles for itself).
+// per lane in flight (4 x 8192 tokens, ragged: 92 us, 5.5 TB/s; with four rows and
+// fewer warps 96 us), in blocks of four warps (of eight: 96 us).  A prompt takes
+// one warp per token; with few tokens (up to four an SM) kTokenWarps share one,
+// and each makes the token's table of angles for itself: 8 tokens 2.8 us (one
+// warp each: 6.9), 512 tokens 4.7 us (7.0), from about 1000 tokens on no gain.
 #pragma once
 
 #include "paged.cuh"

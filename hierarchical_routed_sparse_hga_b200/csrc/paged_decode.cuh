@@ -46,8 +46,8 @@ namespace pdec {
 
 // 12 warps on an SM: with 168 registers a thread a tile of K and of V and the
 // output stay in registers; 16 warps of 128 spill, and read 8 x 32768 slots
-// (bf16, d = 128) in 181 us instead of 168.  Small blocks, so that one merges
-// its warps while another reads.
+// (bf16, 8 heads, d = 128; 1.07 GB) in 187 us instead of 160 (6.7 TB/s).
+// Small blocks, so that one merges its warps while another reads.
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 3;
@@ -99,7 +99,7 @@ struct Work {
 // each head counts that many more where the runs are cut: position p of a
 // head that begins at unit u0 is its unit p - u0 - kHeadUnits.  Without it a
 // block that gets many short sequences is the last to end: 64 sequences of 0
-// to 8190 slots take 186 us instead of 169.
+// to 8190 slots take 183 us instead of 166.
 constexpr int kHeadUnits = 2;
 
 // The runs of the blocks in use: q units each, the first r one more.
@@ -682,9 +682,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // Short caches in one launch: a cluster of nc blocks per (sequence, KV head),
 // each with at most kFewUnits units of its slots; partial results, and the
 // scores for the weights, stay in shared memory and are joined through it.
+// Bound by latency: 1 x 300 slots 5.7 us (with the two kernels above and below
+// 8.6), 1 x 2048 8.2 (10.8), 1 x 4096 12.3 (13.5), 8 x 1024 10.7 (14.5).
 // ---------------------------------------------------------------------------
 constexpr int kMaxC = 8;
-constexpr int kFewUnits = 4;
+constexpr int kFewUnits = 8;
 
 template <typename T, int D>
 struct FewShared {
