@@ -1305,7 +1305,7 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
     const int64_t units = (slots + pdec::Tile<T, D>::kUnit - 1) / pdec::Tile<T, D>::kUnit;
     int nc = 1;
     while (nc < pdec::kMaxC && nc < units && 2 * nc * heads <= pdec::kBlocks) nc *= 2;
-    if (heads <= pdec::kBlocks && units <= int64_t(nc) * pdec::kFewUnits) {
+    if (heads <= pdec::kBlocks && units <= int64_t(nc) * pdec::kFewUnits<T>) {
       const size_t smem = pdec::few_bytes<T, D>(G, accumulate != 0);
       hga_status_t e = ensure_smem(
           reinterpret_cast<const void*>(&pdec::paged_decode_few_kernel<T, D>), smem);

@@ -686,7 +686,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // 8.6), 1 x 2048 8.2 (10.8), 1 x 4096 12.3 (13.5), 8 x 1024 10.7 (14.5).
 // ---------------------------------------------------------------------------
 constexpr int kMaxC = 8;
-constexpr int kFewUnits = 8;
+// a float32 tile takes more instructions: 2 x 2048 slots, 8 units a block, are
+// faster in two launches (17.5 us) than in one (20.5); bf16 the other way
+// round, and from 12 units on two are faster there too (1 x 6144: 15.0, 17.1)
+template <typename T>
+constexpr int kFewUnits = sizeof(T) == 2 ? 8 : 4;
 
 template <typename T, int D>
 struct FewShared {
@@ -700,7 +704,7 @@ struct FewShared {
 template <typename T, int D>
 __host__ __device__ constexpr size_t few_bytes(int G, bool accumulate) {
   return sizeof(FewShared<T, D>) +
-         (accumulate ? size_t(kFewUnits) * Tile<T, D>::kUnit * G * 4 : 0);
+         (accumulate ? size_t(kFewUnits<T>) * Tile<T, D>::kUnit * G * 4 : 0);
 }
 
 // grid (nc, n_kv_heads, batch) in clusters of (nc, 1, 1); the table holds at
