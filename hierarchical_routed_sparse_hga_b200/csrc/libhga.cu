@@ -1384,26 +1384,34 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   int2* counts = static_cast<int2*>(workspace);
   int2* moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) +
                                         align256(size_t(heads) * pev::kMaxC * sizeof(int2)));
-  hga_status_t e = ensure_smem(reinterpret_cast<const void*>(&pev::paged_evict_kernel), smem);
-  if (e != HGA_OK) return e;
-  e = traced_launch(HGA_K_PAGED_EVICT, s, [&] {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
-    lc.blockDim = dim3(pev::kThreads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(nc);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 2;
-    return cudaLaunchKernelEx(&lc, pev::paged_evict_kernel, view, n_slots, pos, int(keep),
-                              int(sinks), int(recent), key_cap, counts, moves);
-  });
+  auto select = [&](auto kernel) -> hga_status_t {
+    hga_status_t e = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != HGA_OK) return e;
+    return traced_launch(HGA_K_PAGED_EVICT, s, [&] {
+      cudaLaunchConfig_t lc = {};
+      lc.gridDim = dim3(unsigned(nc), cfg->n_kv_heads, cfg->batch);
+      lc.blockDim = dim3(pev::kThreads);
+      lc.dynamicSmemBytes = smem;
+      lc.stream = s;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = unsigned(nc);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[1].val.programmaticStreamSerializationAllowed = 1;
+      lc.attrs = attr;
+      lc.numAttrs = 2;
+      return cudaLaunchKernelEx(&lc, kernel, view, n_slots, pos, int(keep), int(sinks),
+                                int(recent), key_cap, counts, moves);
+    });
+  };
+  // few slots on few blocks: the moves in the same launch
+  if (heads * nc <= sm_count() && slots <= int64_t(nc) * pev::kFewSlots)
+    return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
+      return select(pev::paged_evict_kernel<T, D>);
+    });
+  const hga_status_t e = select(pev::paged_evict_kernel<char, 0>);
   if (e != HGA_OK) return e;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
     // one wave: four blocks of moves fit on an SM (8 x 32768 slots cut to 8192:

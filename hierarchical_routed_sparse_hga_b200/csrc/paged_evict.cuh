@@ -23,8 +23,9 @@
 //  3. the moves, each 16-byte piece read and written once.
 // 1 and 2 (paged_evict_kernel) are a chain of short phases; loops are kept
 // rolled where they can be, since each runs once and its instructions are
-// fetched for that one time.  3 (paged_move_kernel) is bound by HBM and wants
-// the whole GPU and other registers, so it is a launch of its own.
+// fetched for that one time.  3 is bound by HBM and wants the whole GPU and
+// other registers, so it is a launch of its own (paged_move_kernel) unless
+// there is little to move.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -39,6 +40,10 @@ namespace cg = cooperative_groups;
 constexpr int kMaxC = 8;  // blocks per cluster, at most (portable size)
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+// A block's share up to which the moves are not a launch of their own: 1 x 1500
+// slots cut to 1024 (a share of 188) 12.2 us against 12.9 and one launch less;
+// 1 x 4096 cut to 2048 (512) 14.6 against 13.4.
+constexpr int kFewSlots = 256;
 constexpr int kKeyCap = 44 * 1024;  // keys in one block's shared memory, at most
 
 // Rank of a slot: tokens that are kept by position above every weight, a NaN
@@ -64,6 +69,7 @@ struct alignas(16) Shared {
   int2 rank[kGroups];  // of the first hole and mover
   int2 warp_sum[kWarps];
   int unlisted, n_equal, bad;
+  int2 n_moves, before[kMaxC + 1];  // the block's holes and movers; of the blocks before each
   // the select's state: keys whose bits from `shift` up exceed prefix's are
   // kept, of those that equal them `need` more (all: every one)
   uint32_t prefix;
@@ -106,11 +112,99 @@ __device__ __forceinline__ int share_begin(int n, int rank, int nc) {
   return min(n, rank * ((((n + nc - 1) / nc) + 3) & ~3));
 }
 
+// Exclusive prefix over a cluster's blocks of their holes and movers, by one
+// warp, from the lanes' own c (lane r: block r's): before[0 .. kMaxC].
+__device__ __forceinline__ void blocks_before(int2 c, int lane, int2* before) {
+  int2 incl = c;
+#pragma unroll
+  for (int o = 1; o < kMaxC; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  if (lane < kMaxC) before[lane + 1] = incl;
+  if (lane == 0) before[0] = make_int2(0, 0);
+}
+
+// The moves of a (sequence, head) of n slots, kPairs at a time per warp, 16
+// bytes per lane and load: warp `worker` of `workers`.  The j-th hole takes the
+// j-th mover; sources lie at or behind slot `keep` and destinations before it,
+// so the moves may run in any order.  list: the blocks' holes and movers;
+// before: their numbers before each of the nc blocks.
+template <typename T, int D>
+__device__ __forceinline__ void move_rows(const PagedView& cache, int h, int n, int nc,
+                                          const int2* list, const int2* before, int worker,
+                                          int workers) {
+  const int lane = threadIdx.x & 31;
+  const int n_moves = before[kMaxC].x;
+  constexpr int kRow = D * int(sizeof(T)) / 16;       // pieces of a row
+  constexpr int kLoads = 4;                           // in flight per lane
+  constexpr int kPairs = kLoads * 32 / (2 * kRow);    // K row and V row of each
+  static_assert(kPairs >= 1 && kPairs <= 32);
+  uint4* kp = static_cast<uint4*>(cache.k);
+  uint4* vp = static_cast<uint4*>(cache.v);
+  auto piece = [&](int2 where) {  // first 16-byte piece of that row
+    return cache.elem(where.x, h, where.y, D) * int(sizeof(T)) / 16;
+  };
+  const int j_step = workers * kPairs;
+  int2 to_where = make_int2(0, 0), from_where = to_where;
+  auto fetch = [&](int j) {  // of the pair that this lane looks after
+    if (lane < kPairs && j + lane < n_moves) {
+      int rh = 0, rm = 0;
+      for (int r = 1; r < nc; ++r) {
+        rh += j + lane >= before[r].x ? 1 : 0;
+        rm += j + lane >= before[r].y ? 1 : 0;
+      }
+      to_where = __ldcg(list + share_begin(n, rh, nc) + (j + lane - before[rh].x));
+      from_where = __ldcg(list + share_begin(n, rm + 1, nc) - 1 - (j + lane - before[rm].y));
+    }
+  };
+  int j0 = worker * kPairs;
+  fetch(j0);
+  for (; j0 < n_moves; j0 += j_step) {
+    const int left = min(kPairs, n_moves - j0);
+    const int64_t src = piece(from_where), dst = piece(to_where);
+    float w = 0.f;
+    int p = 0;
+    int64_t rd = 0;
+    if (lane < left) {
+      const int64_t rs = cache.record(from_where.x, h, from_where.y);
+      rd = cache.record(to_where.x, h, to_where.y);
+      w = cache.weight[rs];
+      p = cache.slot_pos[rs];
+    }
+    fetch(j0 + j_step);
+    uint4 x[kLoads];
+    int64_t to[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * 32 + lane, pair = idx / (2 * kRow), e = idx % (2 * kRow);
+      const int64_t from = __shfl_sync(0xffffffffu, src, pair);
+      to[i] = __shfl_sync(0xffffffffu, dst, pair) + e % kRow;
+      if (pair < left) x[i] = (e < kRow ? kp : vp)[from + e % kRow];
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * 32 + lane, pair = idx / (2 * kRow), e = idx % (2 * kRow);
+      if (pair < left) (e < kRow ? kp : vp)[to[i]] = x[i];
+    }
+    if (lane < left) {
+      cache.weight[rd] = w;
+      cache.slot_pos[rd] = p;
+    }
+  }
+}
+
 // grid (nc, n_kv_heads, batch) in clusters of (nc, 1, 1); dynamic shared
 // memory: Shared, then key_cap keys.  counts: [batch, n_kv_heads, kMaxC] numbers
 // of holes and movers of each block.  moves: [batch, n_kv_heads, capacity]
-// entries of (page, row).
-__global__ void __launch_bounds__(kThreads, 2)
+// entries of (page, row).  D > 0: the moves of rows of D elements of T follow
+// in this launch (counts is not used); D = 0: in paged_move_kernel's.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, D > 0 ? 1 : 2)
     paged_evict_kernel(PagedView cache, const int32_t* __restrict__ n_slots,
                        const int64_t* __restrict__ pos, int keep, int sinks, int recent,
                        int key_cap, int2* __restrict__ counts, int2* __restrict__ moves) {
@@ -135,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the whole cluster reads the same count and leaves here
   const int n = rank == 0 && tid == 0 ? checked_slots(cache, n_slots, b) : n_slots[b];
   const int64_t pair = int64_t(b) * cache.n_kv_heads + h;
-  pdl_launch_dependents();
+  if constexpr (D == 0) pdl_launch_dependents();
   if (n <= keep || int64_t(n) > cache.capacity()) {
-    if (tid == 0) counts[pair * kMaxC + rank] = make_int2(0, 0);
+    if (D == 0 && tid == 0) counts[pair * kMaxC + rank] = make_int2(0, 0);
     return;
   }
   __syncthreads();
@@ -243,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (round == 0 && __syncthreads_or(bad)) {
       // the same for the whole cluster; nothing was written
       if (rank == 0 && tid == 0) latch_status(HGA_ERR_DEVICE_CHECK);
-      if (tid == 0) counts[pair * kMaxC + rank] = make_int2(0, 0);
+      if (D == 0 && tid == 0) counts[pair * kMaxC + rank] = make_int2(0, 0);
       cluster.sync();
       return;
     }
@@ -310,9 +404,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     ties = 0;
     for (int r = 0; r < rank; ++r) ties += *cluster.map_shared_rank(&sh.n_equal, r);
   }
-  // no more of another block's memory is read: done with, but not to be left
-  // before the others are
-  cluster.barrier_arrive();
+  // D = 0: no more of another block's memory is read, but this block's is not
+  // to be left before the others are done with it
+  if constexpr (D == 0) cluster.barrier_arrive();
   int2 at = make_int2(0, 0);  // holes and movers before the chunk
 #pragma unroll 1
   for (int c0 = 0; c0 < n_loc; c0 += kChunk) {
@@ -385,102 +479,45 @@ __global__ void __launch_bounds__(kThreads, 2)
     ties += equals;
     __syncthreads();  // the next chunk overwrites the bits
   }
-  if (tid == 0) counts[pair * kMaxC + rank] = at;
-  cluster.barrier_wait();
+  if constexpr (D == 0) {
+    if (tid == 0) counts[pair * kMaxC + rank] = at;
+    cluster.barrier_wait();
+  } else {
+    if (tid == 0) sh.n_moves = at;
+    cluster.sync();
+    if (warp == 0)
+      blocks_before(lane < nc ? cluster.map_shared_rank(&sh, lane)->n_moves : make_int2(0, 0),
+                    lane, sh.before);
+    __syncthreads();
+    cluster.barrier_arrive();  // no more of another block's memory is read
+    move_rows<T, D>(cache, h, n, nc, moves + pair * cache.capacity(), sh.before,
+                    warp * nc + rank, kWarps * nc);
+    __syncthreads();
+    __threadfence();
+    pdl_launch_dependents();
+    cluster.barrier_wait();
+  }
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;
 
-// grid (x, n_kv_heads, batch): the moves of each (sequence, head) by x blocks,
-// kPairs at a time per warp, 16 bytes per lane and load.  The j-th hole takes
-// the j-th mover; sources lie at or behind slot `keep` and destinations before
-// it, so the moves may run in any order.  nc: blocks of paged_evict_kernel per
-// (sequence, head).
+// grid (x, n_kv_heads, batch): the moves of each (sequence, head) by x blocks;
+// nc: blocks of paged_evict_kernel per (sequence, head)
 template <typename T, int D>
 __global__ void __launch_bounds__(kMoveThreads)
     paged_move_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int nc,
                       const int2* __restrict__ counts, const int2* __restrict__ moves) {
-  __shared__ int2 before[kMaxC + 1];  // holes and movers before each block's share
+  __shared__ int2 before[kMaxC + 1];
   const int h = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t pair_head = int64_t(b) * cache.n_kv_heads + h;
-  const int2* list = moves + pair_head * cache.capacity();
+  const int64_t pair = int64_t(b) * cache.n_kv_heads + h;
   pdl_wait();
-  const int n = n_slots[b];
-  if (warp == 0) {
-    const int2 c = lane < nc ? counts[pair_head * kMaxC + lane] : make_int2(0, 0);
-    int2 incl = c;
-#pragma unroll
-    for (int o = 1; o < kMaxC; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl.x, o);
-      const int y = __shfl_up_sync(0xffffffffu, incl.y, o);
-      if (lane >= o) {
-        incl.x += x;
-        incl.y += y;
-      }
-    }
-    if (lane < kMaxC) before[lane + 1] = incl;
-    if (lane == 0) before[0] = make_int2(0, 0);
-  }
+  if (warp == 0)
+    blocks_before(lane < nc ? counts[pair * kMaxC + lane] : make_int2(0, 0), lane, before);
   __syncthreads();
-  const int n_moves = before[kMaxC].x;
-  constexpr int kRow = D * int(sizeof(T)) / 16;       // pieces of a row
-  constexpr int kLoads = 4;                           // in flight per lane
-  constexpr int kPairs = kLoads * 32 / (2 * kRow);    // K row and V row of each
-  static_assert(kPairs >= 1 && kPairs <= 32);
-  uint4* kp = static_cast<uint4*>(cache.k);
-  uint4* vp = static_cast<uint4*>(cache.v);
-  auto piece = [&](int2 where) {  // first 16-byte piece of that row
-    return cache.elem(where.x, h, where.y, D) * int(sizeof(T)) / 16;
-  };
-  const int j_step = kMoveWarps * int(gridDim.x) * kPairs;
-  int2 to_where = make_int2(0, 0), from_where = to_where;
-  auto fetch = [&](int j) {  // of the pair that this lane looks after
-    if (lane < kPairs && j + lane < n_moves) {
-      int rh = 0, rm = 0;
-      for (int r = 1; r < nc; ++r) {
-        rh += j + lane >= before[r].x ? 1 : 0;
-        rm += j + lane >= before[r].y ? 1 : 0;
-      }
-      to_where = list[share_begin(n, rh, nc) + (j + lane - before[rh].x)];
-      from_where = list[share_begin(n, rm + 1, nc) - 1 - (j + lane - before[rm].y)];
-    }
-  };
-  int j0 = (warp * int(gridDim.x) + int(blockIdx.x)) * kPairs;
-  fetch(j0);
-  for (; j0 < n_moves; j0 += j_step) {
-    const int left = min(kPairs, n_moves - j0);
-    const int64_t src = piece(from_where), dst = piece(to_where);
-    float w = 0.f;
-    int p = 0;
-    int64_t rd = 0;
-    if (lane < left) {
-      const int64_t rs = cache.record(from_where.x, h, from_where.y);
-      rd = cache.record(to_where.x, h, to_where.y);
-      w = cache.weight[rs];
-      p = cache.slot_pos[rs];
-    }
-    fetch(j0 + j_step);
-    uint4 x[kLoads];
-    int64_t to[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = i * 32 + lane, pair = idx / (2 * kRow), e = idx % (2 * kRow);
-      const int64_t from = __shfl_sync(0xffffffffu, src, pair);
-      to[i] = __shfl_sync(0xffffffffu, dst, pair) + e % kRow;
-      if (pair < left) x[i] = (e < kRow ? kp : vp)[from + e % kRow];
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = i * 32 + lane, pair = idx / (2 * kRow), e = idx % (2 * kRow);
-      if (pair < left) (e < kRow ? kp : vp)[to[i]] = x[i];
-    }
-    if (lane < left) {
-      cache.weight[rd] = w;
-      cache.slot_pos[rd] = p;
-    }
-  }
+  move_rows<T, D>(cache, h, n_slots[b], nc, moves + pair * cache.capacity(), before,
+                  warp * int(gridDim.x) + int(blockIdx.x), kMoveWarps * int(gridDim.x));
   // as at the end of paged_join_kernel
   __syncthreads();
   __threadfence();

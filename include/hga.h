@@ -591,7 +591,7 @@ HGA_API size_t hga_paged_evict_workspace_size(const hga_config_t* cfg, const hga
  * sinks + recent <= keep.  A sequence with more than `keep` slots that has a
  * page out of range among them is left untouched (HGA_ERR_DEVICE_CHECK is
  * latched).  workspace as above: at least hga_paged_evict_workspace_size()
- * bytes.  Two launches.
+ * bytes.  One launch for few slots, two otherwise.
  */
 HGA_API hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages_t* cache,
                                      const int32_t* n_slots, const int64_t* pos, int32_t keep,

@@ -547,6 +547,7 @@ EVICT = [
     (dict(lens=(1000, 513, 512), ps=16, paired=True), 512, 4, 100),
     (dict(lens=(1000, 77), dtype="f32", d=64, Hkv=5, G=1, ps=128), 70, 0, 70),
     (dict(lens=(257, 600), dtype="f32", ps=32), 256, 128, 128),
+    (dict(lens=(500, 90), d=64, G=2, paired=True), 80, 4, 16),
     (dict(lens=(20000, 9000), Hkv=1, d=64, ps=64), 8192, 4, 64),
     (dict(lens=(5000,) * 3, d=64, ps=16, paired=True), 4990, 4, 64),
     (dict(lens=(70000,), Hkv=1, d=64, ps=256), 33333, 10, 1000),
