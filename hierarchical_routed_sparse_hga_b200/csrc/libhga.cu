@@ -1414,9 +1414,13 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   const hga_status_t e = select(pev::paged_evict_kernel<char, 0>);
   if (e != HGA_OK) return e;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    // one wave: four blocks of moves fit on an SM (8 x 32768 slots cut to 8192:
-    // 108 us, with eight 110, with six 120); at least one per (sequence, head)
-    const int64_t x = std::max<int64_t>(1, 4 * int64_t(sm_count()) / heads);
+    // One wave: four blocks of moves fit on an SM (8 x 32768 slots cut to 8192:
+    // 108 us, with eight 110, with twelve 113; 53 x 2479, one KV head: 16.3, 18.7).
+    // Several long sequences may differ much in length, and then more and
+    // smaller blocks even out who has what to move (31 x 4 heads, up to 20701
+    // slots: 62 us with eight an SM, 77 with four).
+    const int per_sm = cfg->batch >= 4 && slots >= 8192 ? 8 : 4;
+    const int64_t x = std::max<int64_t>(1, per_sm * int64_t(sm_count()) / heads);
     dim3 grid(unsigned(std::min<int64_t>(x, (slots + 63) / 64)), cfg->n_kv_heads, cfg->batch);
     return traced_launch(HGA_K_PAGED_MOVE, s, [&] {
       return launch_pdl(pev::paged_move_kernel<T, D>, grid, dim3(pev::kMoveThreads), 0, s, view,
