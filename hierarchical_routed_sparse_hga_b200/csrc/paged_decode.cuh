@@ -29,9 +29,13 @@
 // merged through shared memory in warp order.  All orders are fixed, so
 // results are deterministic.
 //
-// Precision.  Statistics and sums are float32.  P enters its product as two
-// bf16 parts (high and remainder, 16 bits): one part alone would add an error
-// as large as the rounding of a bf16 output.  Float32 operands are split into
+// Precision.  Statistics and sums are float32.  P enters its product as three
+// bf16 parts, which hold all of its 24 bits (two parts hold 16: 1 us of 163
+// less at 8 x 32768 slots, and errors of 2^-17).  The matrix unit cuts its sums
+// off instead of rounding them, so it forms short ones only (16 slots, 16 or 32
+// elements of d) and additions sum those: sums of bf16 products over 64 tiles
+// come out 0.9 * 2^-24 off (root mean square), 4.3 in the unit throughout, for
+// 1 us more.  Float32 operands are split into
 // two tf32 parts and the three largest of the four products are summed: each
 // product is good to 2^-19, where one part alone is good to 2^-9.
 #pragma once
@@ -160,9 +164,12 @@ struct Split {
   }
 };
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
+// the upper 16 bits of x[0] and x[1] as a pair of bf16 numbers; rest: what they leave
+__device__ __forceinline__ uint32_t bf16_parts(const float (&x)[2], float (&rest)[2]) {
+  const uint32_t a = __float_as_uint(x[0]), b = __float_as_uint(x[1]);
+  rest[0] = x[0] - __uint_as_float(a & 0xffff0000u);
+  rest[1] = x[1] - __uint_as_float(b & 0xffff0000u);
+  return __byte_perm(a, b, 0x7632);
 }
 
 // one warp's running softmax over its slots: reference m and sum l of head
@@ -191,8 +198,10 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float s
                                            float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2]) {
   using L = Tile<T, D>;
   float acc[L::kSlabs][L::kNt][2] = {};
+  // The matrix unit sums 32 (float32: 16) elements of d at a time, additions
+  // sum those.  (All 128 in the unit: scores 2.5 * 2^-24 short in the mean instead
+  // of 0.7; 16 at a time 0.4, but 2.5 us more at 8 x 32768 slots.)
   if constexpr (L::kBf16) {
-    float c[L::kSlabs][L::kNt][4] = {};
 #pragma unroll
     for (int j = 0; j < L::kKc; ++j) {
       const uint4 a = q[4 * j];
@@ -201,20 +210,16 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float s
 #pragma unroll
         for (int nt = 0; nt < L::kNt; ++nt) {
           const uint4 k = kr[sl][nt][j];
-          mma_bf16(c[sl][nt], a.x, 0u, a.y, 0u, k.x, k.y);
-          mma_bf16(c[sl][nt], a.z, 0u, a.w, 0u, k.z, k.w);
+          float c0[4] = {};
+          mma_bf16(c0, a.x, 0u, a.y, 0u, k.x, k.y);
+          mma_bf16(c0, a.z, 0u, a.w, 0u, k.z, k.w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[sl][nt][i] += c0[i];
         }
     }
-#pragma unroll
-    for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-      for (int nt = 0; nt < L::kNt; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[sl][nt][i] = c[sl][nt][i];
   } else {
-    // The matrix unit cuts its sums off instead of rounding them: it sums 16
-    // elements of d at a time, additions sum those (4 x 16384 slots come out
-    // 5.3e-7 off, plain float32 sums 1.5e-6, sums in the unit alone 2.8e-6).
+    // (4 x 16384 slots come out 5.3e-7 off, plain float32 sums 1.5e-6, sums in
+    // the unit alone 2.8e-6)
 #pragma unroll
     for (int j = 0; j < L::kKc; ++j) {
       const uint4 a = q[4 * j], a_lo = q[Queries<T, D>::kLo + 4 * j];
@@ -282,12 +287,14 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
         acc.l += p[nt][i];
       }
     if constexpr (L::kBf16) {
-      uint32_t hi[2], lo[2];
+      // p = hi + mid + lo in three bf16 numbers of 8 bits, each cut off: exact
+      uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        hi[nt] = bf16_pair(p[nt][0], p[nt][1]);
-        lo[nt] = bf16_pair(p[nt][0] - __uint_as_float(hi[nt] << 16),
-                           p[nt][1] - __uint_as_float(hi[nt] & 0xffff0000u));
+        float r[2];
+        hi[nt] = bf16_parts(p[nt], r);
+        mid[nt] = bf16_parts(r, r);
+        lo[nt] = bf16_parts(r, r);
       }
 #pragma unroll
       for (int x = 0; x < L::kVc; ++x)
@@ -301,8 +308,12 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
           const uint32_t a1 = __byte_perm(word(0), word(1), 0x7632);
           const uint32_t a2 = __byte_perm(word(2), word(3), 0x5410);
           const uint32_t a3 = __byte_perm(word(2), word(3), 0x7632);
-          mma_bf16(acc.o[x * 4 + w], a0, a1, a2, a3, lo[0], lo[1]);
-          mma_bf16(acc.o[x * 4 + w], a0, a1, a2, a3, hi[0], hi[1]);
+          float c[4] = {};  // added below: see score_tile
+          mma_bf16(c, a0, a1, a2, a3, lo[0], lo[1]);
+          mma_bf16(c, a0, a1, a2, a3, mid[0], mid[1]);
+          mma_bf16(c, a0, a1, a2, a3, hi[0], hi[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc.o[x * 4 + w][i] += c[i];
         }
     } else {
       const Split p0(__float_as_uint(p[0][0]), true), p1(__float_as_uint(p[0][1]), true);
