@@ -4,7 +4,7 @@
 // prepare.cuh).  Memory-bound: each projection element is read once and
 // written once.
 //
-// Warps work on their own, without block barriers: the chain in front of a
+// Warps work on their own, without block barriers but the last: the chain in front of a
 // token's rows (counts, page, angles) takes longer than the rows themselves,
 // so what counts is that many tokens are at different points of it: two rows
 // per lane in flight (4 x 8192 tokens, ragged: 92 us, 5.5 TB/s; with four rows and
@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         }
     }
   }
-  // the next kernel on the stream may read Q before its own wait (the routing
-  // does): let it start only once every store is visible
+  // The next kernel on the stream may read Q before its own wait (the routing
+  // does).  The first warp's trigger counts for the whole block, so it comes
+  // after the last one's stores.
+  __syncthreads();
   __threadfence();
   pdl_launch_dependents();
 }
