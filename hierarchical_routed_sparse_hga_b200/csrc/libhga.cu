@@ -1192,8 +1192,9 @@ struct PagedWork {
   size_t bytes;
 };
 
-// The decode workspace: the blocks' runs, the partial results,
-// and (with weights) a score per slot and query head; 256-byte sections.
+// The decode workspace: the blocks' runs, the partial results, and (with
+// weights) maximum and sum of every query head and a score per slot and query
+// head; 256-byte sections.
 PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumulate, void* base) {
   const int d = cfg->head_dim, G = cfg->n_q_heads / cfg->n_kv_heads;
   const size_t runs_bytes = align256(sizeof(pdec::Run) * pdec::kBlocks);
@@ -1205,17 +1206,22 @@ PagedWork paged_work(const hga_config_t* cfg, const hga_pages_t* c, bool accumul
   const size_t head_units =
       (size_t(c->max_pages) * c->page_size + unit - 1) / unit + pdec::kHeadUnits;
   const size_t slots = head_units * unit;
+  const size_t stat_bytes =
+      accumulate ? align256(size_t(cfg->batch) * cfg->n_q_heads * sizeof(float2)) : 0;
   const size_t score_bytes =
       accumulate ? align256(slots * cfg->batch * cfg->n_q_heads * 4) : 0;
   char* p = static_cast<char*>(base);
   PagedWork w = {};
   // the kernels count units in 32 bits
   if (head_units * cfg->batch * cfg->n_kv_heads > 0x7fffffff) return w;
-  w.bytes = runs_bytes + part_bytes + score_bytes;
+  w.bytes = runs_bytes + part_bytes + stat_bytes + score_bytes;
   if (base) {
     w.work.runs = reinterpret_cast<pdec::Run*>(p);
     w.work.part = reinterpret_cast<float*>(p + runs_bytes);
-    if (accumulate) w.work.scores = reinterpret_cast<float*>(p + runs_bytes + part_bytes);
+    if (accumulate) {
+      w.work.stats = reinterpret_cast<float2*>(p + runs_bytes + part_bytes);
+      w.work.scores = reinterpret_cast<float*>(p + runs_bytes + part_bytes + stat_bytes);
+    }
   }
   return w;
 }
@@ -1294,7 +1300,7 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
   if (ws_bytes < need) return HGA_ERR_WORKSPACE;
   const PagedView view = paged_view(cfg, cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const float scale_log2 = cfg->scale * 1.4426950408889634f;
+  const pdec::Scale scale(cfg->scale);
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
     const int G = cfg->n_q_heads / cfg->n_kv_heads;
     // A table so narrow that one cluster per (sequence, KV head), all clusters
@@ -1327,13 +1333,13 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
         lc.numAttrs = 2;
         return cudaLaunchKernelEx(&lc, pdec::paged_decode_few_kernel<T, D>, view,
                                   static_cast<const T*>(q), n_slots, G, int(accumulate),
-                                  scale_log2, static_cast<T*>(o), lse);
+                                  scale, static_cast<T*>(o), lse);
       });
     }
     const pdec::Work work = paged_work(cfg, cache, accumulate != 0, workspace).work;
     hga_status_t e = traced_launch(HGA_K_PAGED_DECODE, s, [&] {
       return launch_pdl(pdec::paged_decode_kernel<T, D>, dim3(pdec::kBlocks), dim3(pdec::kThreads),
-          0, s, view, static_cast<const T*>(q), n_slots, cfg->batch, G, scale_log2,
+          0, s, view, static_cast<const T*>(q), n_slots, cfg->batch, G, scale,
           static_cast<T*>(o), lse, work);
     });
     if (e != HGA_OK) return e;
@@ -1341,7 +1347,7 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
     dim3 grid(pdec::kBlocks * G + adders);
     return traced_launch(HGA_K_PAGED_JOIN, s, [&] {
       return launch_pdl(pdec::paged_join_kernel<T, D>, grid, dim3(pdec::kJoinThreads), 0, s, view,
-          n_slots, G, adders, static_cast<T*>(o), lse, work);
+          n_slots, G, adders, scale, static_cast<T*>(o), lse, work);
     });
   });
 }

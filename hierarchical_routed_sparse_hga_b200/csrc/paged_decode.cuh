@@ -1,6 +1,10 @@
 // Attention of one new token per sequence over its paged cache.
 //
-//   s_j = scale q.k_j,  O = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m)   (s in base 2)
+//   x_j = q.k_j,  p_j = 2^((x_j - m) scale / ln 2),  O = sum_j p_j v_j / sum_j p_j,
+//   LSE = m scale + ln sum_j p_j
+//
+// (the scale comes after the difference: two scores that are close keep their
+// distance, and LSE is rounded once)
 //
 // Every key and value is read once and meets G <= 8 queries: 4 G flops for
 // the 4 (bf16) or 8 (float32) bytes of a K and a V element, far below what the
@@ -42,6 +46,8 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
 
@@ -57,11 +63,18 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 3;
 constexpr int kBlocks = 148 * kBlocksPerSm;  // of the B200's 148 SMs
 constexpr int kMaxG = 8;
-constexpr float kLn2 = 0.6931471805599453f;
-// the reference point of the running softmax moves only when a score exceeds
-// it by more than this (in base 2): the weights stay below 2^8, no precision
-// is lost in float32, and nearly every tile is spared the rescaling
-constexpr float kSlack = 8.f;
+
+// What a product q.k counts.  The reference point of the running softmax moves
+// only when a product exceeds it by more than `slack`, 8 in base 2: the
+// weights stay below 2^8, no precision is lost in float32, and nearly every
+// tile is spared the rescaling.
+struct Scale {
+  float score;  // of the products in the scores
+  float log2;   // the same in base 2
+  float slack;  // finite, so that a reference of -inf always moves
+  explicit Scale(float scale)
+      : score(scale), log2(scale * 1.4426950408889634f), slack(std::min(8.f / log2, 1e37f)) {}
+};
 
 template <typename T, int D>
 struct Tile {
@@ -95,7 +108,8 @@ struct alignas(16) Run {
 struct Work {
   Run* runs;        // [kBlocks]
   float* part;      // [2 * kBlocks][G * (D + 2)]: m[G], l[G], o[G][D] of an incomplete piece
-  float* scores;    // [units][kUnit / kSlots][G][kSlots], in base 2; nullptr: not kept
+  float* scores;    // [units][kUnit / kSlots][G][kSlots], q.k; nullptr: not kept
+  float2* stats;    // [batch * n_q_heads] (maximum, sum) of the heads in one piece, with scores
 };
 
 // A piece costs about as much as kHeadUnits units on top of those it has (its
@@ -191,13 +205,18 @@ struct Queries {
   alignas(16) T row[kParts][kMaxG][kRow];
 };
 
-// Scores of the tile in kr (base 2), by lane: heads lane / 4, two slots per
-// column of 8.  q: this lane's first piece of its query row.
+// Products q.k of the tile in kr, by lane: heads lane / 4, two slots per column
+// of 8.  q: this lane's first piece of its query row.
 template <typename T, int D, typename KR>
-__device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float scale_log2,
+__device__ __forceinline__ void score_tile(const KR& kr, const uint4* q,
                                            float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2]) {
   using L = Tile<T, D>;
-  float acc[L::kSlabs][L::kNt][2] = {};
+#pragma unroll
+  for (int sl = 0; sl < L::kSlabs; ++sl)
+#pragma unroll
+    for (int nt = 0; nt < L::kNt; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[sl][nt][i] = 0.f;
   // The matrix unit sums 32 (float32: 16) elements of d at a time, additions
   // sum those.  (All 128 in the unit: scores 2.5 * 2^-24 short in the mean instead
   // of 0.7; 16 at a time 0.4, but 2.5 us more at 8 x 32768 slots.)
@@ -214,7 +233,7 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float s
           mma_bf16(c0, a.x, 0u, a.y, 0u, k.x, k.y);
           mma_bf16(c0, a.z, 0u, a.w, 0u, k.z, k.w);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) acc[sl][nt][i] += c0[i];
+          for (int i = 0; i < 2; ++i) s[sl][nt][i] += c0[i];
         }
     }
   } else {
@@ -234,35 +253,29 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q, float s
         mma_tf32(c, a.z, 0u, a.w, 0u, kz.lo, kw.lo);
         mma_tf32(c, a.x, 0u, a.y, 0u, kx.hi, ky.hi);
         mma_tf32(c, a.z, 0u, a.w, 0u, kz.hi, kw.hi);
-        acc[sl][0][0] += c[0];
-        acc[sl][0][1] += c[1];
+        s[sl][0][0] += c[0];
+        s[sl][0][1] += c[1];
       }
     }
   }
-#pragma unroll
-  for (int sl = 0; sl < L::kSlabs; ++sl)
-#pragma unroll
-    for (int nt = 0; nt < L::kNt; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) s[sl][nt][i] = acc[sl][nt][i] * scale_log2;
 }
 
 // Adds the tile in vr, with its scores, to the running softmax.
 template <typename T, int D, typename VR>
 __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
                                          float (&s)[Tile<T, D>::kSlabs][Tile<T, D>::kNt][2],
-                                         int lane) {
+                                         const Scale& scale, int lane) {
   using L = Tile<T, D>;
   float top = -INFINITY;
 #pragma unroll
   for (int sl = 0; sl < L::kSlabs; ++sl)
 #pragma unroll
     for (int nt = 0; nt < L::kNt; ++nt) top = fmaxf(top, fmaxf(s[sl][nt][0], s[sl][nt][1]));
-  if (__any_sync(0xffffffffu, top > acc.m + kSlack)) {
+  if (__any_sync(0xffffffffu, top > acc.m + scale.slack)) {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     top = fmaxf(top, acc.m);
-    const float a = top == -INFINITY ? 1.f : exp2f(acc.m - top);
+    const float a = top == -INFINITY ? 1.f : exp2f((acc.m - top) * scale.log2);
     acc.m = top;
     acc.l *= a;
     const float a0 = __shfl_sync(0xffffffffu, a, (lane & 3) * 8);
@@ -283,7 +296,7 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float x = s[sl][nt][i];
-        p[nt][i] = x == -INFINITY ? 0.f : sm100::ex2_approx(x - acc.m);
+        p[nt][i] = x == -INFINITY ? 0.f : sm100::ex2_approx((x - acc.m) * scale.log2);
         acc.l += p[nt][i];
       }
     if constexpr (L::kBf16) {
@@ -337,17 +350,22 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
 
 // what a partial result (maximum m, sum l) counts in one with maximum M; one
 // that attended to nothing counts nothing
-__device__ __forceinline__ float part_scale(float m, float l, float M) {
-  return m == -INFINITY && l == 0.f ? 0.f : exp2f(m - M);
+__device__ __forceinline__ float part_scale(float m, float l, float M, const Scale& scale) {
+  return m == -INFINITY && l == 0.f ? 0.f : exp2f((m - M) * scale.log2);
 }
 
-// the final output and log-sum-exp (base 2) of a sum
+// the final output and log-sum-exp of a sum
 template <typename T>
 __device__ __forceinline__ T final_out(float out, float sum) {
   return from_float<T>(sum == 0.f ? 0.f : out / sum);
 }
-__device__ __forceinline__ float final_lse2(float M, float sum) {
-  return sum == 0.f ? -INFINITY : M + log2f(sum);
+__device__ __forceinline__ float final_lse(float M, float sum, const Scale& scale) {
+  return sum == 0.f ? -INFINITY : fmaf(M, scale.score, logf(sum));
+}
+// what add_weights takes of a query head's maximum and sum; attended to nothing:
+// no weight
+__device__ __forceinline__ float2 head_stat(float M, float sum) {
+  return sum == 0.f ? make_float2(0.f, 0.f) : make_float2(M, 1.f / sum);
 }
 
 // One block's share of a (sequence, KV head): its warps take the tiles of slots
@@ -356,7 +374,7 @@ __device__ __forceinline__ float final_lse2(float M, float sum) {
 template <typename T, int D>
 __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __restrict__ table,
                                        int h, const T* __restrict__ q, int G, int t_lo, int t_hi,
-                                       float scale_log2, float* score_out, Queries<T, D>& qs,
+                                       const Scale& scale, float* score_out, Queries<T, D>& qs,
                                        Acc<T, D>& acc) {
   using L = Tile<T, D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -451,7 +469,7 @@ __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __
   for (int tile = 0; tile < tiles; ++tile) {
     asm volatile("" : "+l"(qp));  // read again for every tile
     float s[L::kSlabs][L::kNt][2];
-    score_tile<T, D>(kr, qp, scale_log2, s);
+    score_tile<T, D>(kr, qp, s);
 #pragma unroll
     for (int sl = 0; sl < L::kSlabs; ++sl)
 #pragma unroll
@@ -475,7 +493,7 @@ __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __
       locate(tile + 1);
       load_k();
     }
-    add_tile<T, D>(acc, vr, s, lane);
+    add_tile<T, D>(acc, vr, s, scale, lane);
     if (more) load_v();
   }
 }
@@ -486,7 +504,8 @@ __device__ __forceinline__ void attend(const PagedView& cache, const int32_t* __
 template <typename T, int D, typename F>
 __device__ __forceinline__ void merge_warps(const Acc<T, D>& acc, float (&wo)[kWarps][kMaxG][D],
                                             float (&wm)[kWarps][kMaxG],
-                                            float (&wl)[kWarps][kMaxG], int G, F&& f) {
+                                            float (&wl)[kWarps][kMaxG], int G,
+                                            const Scale& scale, F&& f) {
   using L = Tile<T, D>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n8 = lane >> 2, q4 = lane & 3;
@@ -517,7 +536,7 @@ __device__ __forceinline__ void merge_warps(const Acc<T, D>& acc, float (&wo)[kW
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][g]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float a = part_scale(wm[w][g], wl[w][g], M);
+      const float a = part_scale(wm[w][g], wl[w][g], M, scale);
       sum = fmaf(a, wl[w][g], sum);
       out = fmaf(a, wo[w][g][e], out);
     }
@@ -525,14 +544,17 @@ __device__ __forceinline__ void merge_warps(const Acc<T, D>& acc, float (&wo)[kW
   }
 }
 
-// weight[slot] += sum_g 2^(s_g - lse_g) of slots [t_lo, t_hi), by `threads`
-// threads; scores as attend() stored them, lse in base 2 (+inf: no weight).  An
-// addition in memory, not a load and a store: two sequences may share a page.
+// weight[slot] += sum_g p_g / (sum of head g) of slots [t_lo, t_hi), by `threads`
+// threads; score: the products as attend() stored them, stat: each head's maximum and
+// 1 / sum.  (By way of LSE a weight would be off by LSE's rounding, all of a head's
+// the same way.)  An addition in memory, not a load and a store: two sequences
+// may share a page.
 template <typename T, int D>
 __device__ __forceinline__ void add_weights(const PagedView& cache,
                                             const int32_t* __restrict__ table, int h, int G,
                                             int t_lo, int t_hi, const float* score,
-                                            const float* lse, int thread, int threads) {
+                                            const float2* stat, const Scale& scale, int thread,
+                                            int threads) {
   using L = Tile<T, D>;
   // four slots at a time: they lie on one page, and their records on 16 bytes
 #pragma unroll 2
@@ -543,10 +565,11 @@ __device__ __forceinline__ void add_weights(const PagedView& cache,
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int g = 0; g < G; ++g) {
       const float4 x = *reinterpret_cast<const float4*>(s + g * L::kSlots);
-      w.x += exp2f(x.x - lse[g]);
-      w.y += exp2f(x.y - lse[g]);
-      w.z += exp2f(x.z - lse[g]);
-      w.w += exp2f(x.w - lse[g]);
+      const float2 of = stat[g];
+      w.x = fmaf(sm100::ex2_approx((x.x - of.x) * scale.log2), of.y, w.x);
+      w.y = fmaf(sm100::ex2_approx((x.y - of.x) * scale.log2), of.y, w.y);
+      w.z = fmaf(sm100::ex2_approx((x.z - of.x) * scale.log2), of.y, w.z);
+      w.w = fmaf(sm100::ex2_approx((x.w - of.x) * scale.log2), of.y, w.w);
     }
     float* dst = &cache.weight[cache.record(page, h, cache.row_of(t))];
     if (t + 4 <= t_hi) {
@@ -578,7 +601,7 @@ struct Shared {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     paged_decode_kernel(PagedView cache, const T* __restrict__ q,
-                        const int32_t* __restrict__ n_slots, int batch, int G, float scale_log2,
+                        const int32_t* __restrict__ n_slots, int batch, int G, Scale scale,
                         T* __restrict__ o, float* __restrict__ lse, Work work) {
   using L = Tile<T, D>;
   __shared__ Shared<T, D> sh;
@@ -684,14 +707,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     {
       const int b = sh.seq, h = sh.head;
       attend<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h,
-                   q + (int64_t(b) * n_kv + h) * G * D, G, sh.t_lo, sh.t_hi, scale_log2,
+                   q + (int64_t(b) * n_kv + h) * G * D, G, sh.t_lo, sh.t_hi, scale,
                    work.scores ? work.scores + int64_t(sh.first) * L::kUnit * G : nullptr, sh.q, acc);
     }
     const int64_t row0 = (int64_t(sh.seq) * n_kv + sh.head) * G;
-    merge_warps(acc, sh.wo, sh.wm, sh.wl, G, [&](int g, int e, float M, float sum, float out) {
+    merge_warps(acc, sh.wo, sh.wm, sh.wl, G, scale, [&](int g, int e, float M, float sum, float out) {
       if (sh.part < 0) {
         o[(row0 + g) * D + e] = final_out<T>(out, sum);
-        if (e == 0) lse[row0 + g] = final_lse2(M, sum) * kLn2;
+        if (e == 0) {
+          lse[row0 + g] = final_lse(M, sum, scale);
+          if (work.stats) work.stats[row0 + g] = make_float2(M, sum);
+        }
       } else {
         float* part = work.part + int64_t(sh.part) * G * (D + 2);
         part[2 * G + g * D + e] = out;
@@ -724,7 +750,7 @@ struct FewShared {
   float wo[kWarps][kMaxG][D];
   float wm[kWarps][kMaxG], wl[kWarps][kMaxG];
   float po[kMaxG][D], pm[kMaxG], pl[kMaxG];  // the block's partial result
-  float head_lse[kMaxG];
+  float2 stat[kMaxG];
 };
 // dynamic shared memory: FewShared, then (accumulate) the scores of kFewUnits units
 template <typename T, int D>
@@ -739,7 +765,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     paged_decode_few_kernel(PagedView cache, const T* __restrict__ q,
                             const int32_t* __restrict__ n_slots, int G, int accumulate,
-                            float scale_log2, T* __restrict__ o, float* __restrict__ lse) {
+                            Scale scale, T* __restrict__ o, float* __restrict__ lse) {
   using L = Tile<T, D>;
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -759,9 +785,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const int t_lo = rank * head_units / nc * L::kUnit;
   const int t_hi = min(n, (rank + 1) * head_units / nc * L::kUnit);
   Acc<T, D> acc;
-  attend<T, D>(cache, table, h, q + row0 * D, G, t_lo, t_hi, scale_log2,
+  attend<T, D>(cache, table, h, q + row0 * D, G, t_lo, t_hi, scale,
                accumulate ? scores - int64_t(t_lo) * G : nullptr, sh.q, acc);
-  merge_warps(acc, sh.wo, sh.wm, sh.wl, G, [&](int g, int e, float M, float sum, float out) {
+  merge_warps(acc, sh.wo, sh.wm, sh.wl, G, scale, [&](int g, int e, float M, float sum, float out) {
     sh.po[g][e] = out;
     if (e == 0) {
       sh.pm[g] = M;
@@ -771,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   cluster.sync();
 
   // every block joins its share of the output elements, in block order; a
-  // thread per query head forms the log-sum-exp for the weights
+  // thread per query head forms its maximum and sum for the weights
   auto stats = [&](int g, float& M, float& sum) {
     float m[kMaxC], l[kMaxC];
     M = -INFINITY;
@@ -786,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
 #pragma unroll
     for (int r = 0; r < kMaxC; ++r)
-      if (r < nc) sum = fmaf(part_scale(m[r], l[r], M), l[r], sum);
+      if (r < nc) sum = fmaf(part_scale(m[r], l[r], M, scale), l[r], sum);
   };
   for (int i = rank * kThreads + tid; i < G * D; i += nc * kThreads) {
     const int g = i / D, e = i % D;
@@ -794,20 +820,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     stats(g, M, sum);
     for (int r = 0; r < nc; ++r) {
       const FewShared<T, D>* peer = cluster.map_shared_rank(&sh, r);
-      out = fmaf(part_scale(peer->pm[g], peer->pl[g], M), peer->po[g][e], out);
+      out = fmaf(part_scale(peer->pm[g], peer->pl[g], M, scale), peer->po[g][e], out);
     }
     o[(row0 + g) * D + e] = final_out<T>(out, sum);
-    if (e == 0) lse[row0 + g] = final_lse2(M, sum) * kLn2;
+    if (e == 0) lse[row0 + g] = final_lse(M, sum, scale);
   }
   if (accumulate) {
     if (tid < G) {
       float M, sum;
       stats(tid, M, sum);
-      sh.head_lse[tid] = sum == 0.f ? INFINITY : M + log2f(sum);
+      sh.stat[tid] = head_stat(M, sum);
     }
     __syncthreads();
-    add_weights<T, D>(cache, table, h, G, t_lo, t_hi, scores - int64_t(t_lo) * G, sh.head_lse, tid,
-                      kThreads);
+    add_weights<T, D>(cache, table, h, G, t_lo, t_hi, scores - int64_t(t_lo) * G, sh.stat, scale,
+                      tid, kThreads);
   }
   __syncthreads();
   __threadfence();  // as at the end of paged_join_kernel
@@ -818,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // ---------------------------------------------------------------------------
 // Joins the incomplete pieces, and adds the weights.  The first `adders` blocks
 // (accumulate: kBlocks, one per block of the decode kernel, over the same run;
-// else 0) form the LSE of the G heads and add sum_g 2^(s_g - LSE_g) to the
-// weights from the scores that the decode kernel left, in L2 for the most part.
+// else 0) form the maxima and sums of the G heads and add to the weights from the
+// scores that the decode kernel left, in L2 for the most part.
 // At most one head goes on from each block's run to the next, so the other
 // kBlocks * G blocks join: block (c, g) the pieces of query head g of the head
 // that begins in block c's last piece, in block order.  Most of them have
@@ -845,11 +871,12 @@ struct Pieces {
 };
 
 // maximum and sum over the pieces for head g, by the kLanes lanes of a warp
-// that share it (sub: which of them); scale[i] (if not nullptr) receives what
+// that share it (sub: which of them); counts[i] (if not nullptr) receives what
 // piece i counts
 template <int kLanes>
-__device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, int sub, float& M,
-                                           float& sum, float* scale) {
+__device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, int sub,
+                                           const Scale& scale, float& M, float& sum,
+                                           float* counts) {
   M = -INFINITY;
 #pragma unroll 4
   for (int i = sub; i < pieces.n; i += kLanes) M = fmaxf(M, pieces[i][g]);
@@ -858,9 +885,9 @@ __device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, i
   sum = 0.f;
 #pragma unroll 4
   for (int i = sub; i < pieces.n; i += kLanes) {
-    const float l = pieces[i][G + g], a = part_scale(pieces[i][g], l, M);
+    const float l = pieces[i][G + g], a = part_scale(pieces[i][g], l, M, scale);
     sum = fmaf(a, l, sum);
-    if (scale) scale[i] = a;
+    if (counts) counts[i] = a;
   }
 #pragma unroll
   for (int w = kLanes / 2; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -869,12 +896,12 @@ __device__ __forceinline__ void join_stats(const Pieces& pieces, int G, int g, i
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     paged_join_kernel(PagedView cache, const int32_t* __restrict__ n_slots, int G, int adders,
-                      T* __restrict__ o, float* __restrict__ lse, Work work) {
+                      Scale scale, T* __restrict__ o, float* __restrict__ lse, Work work) {
   using L = Tile<T, D>;
   constexpr int kRows = kJoinThreads / D;
   __shared__ float red[kRows][D];
-  __shared__ float scale[kBlocks], total;
-  __shared__ float head_lse[kJoinThreads / 32][kMaxG];
+  __shared__ float counts[kBlocks], total;
+  __shared__ float2 stat[kJoinThreads / 32][kMaxG];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_kv = cache.n_kv_heads;
   pdl_wait();
@@ -913,20 +940,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       const int64_t row0 = (int64_t(b) * n_kv + h) * G;
       {  // four lanes per query head
         const int g = min(lane / 4, G - 1);
-        float x;
+        float M, sum;
         if (pieces.n > 1) {
-          float M, sum;
-          join_stats<4>(pieces, G, g, lane % 4, M, sum, nullptr);
-          x = final_lse2(M, sum);
+          join_stats<4>(pieces, G, g, lane % 4, scale, M, sum, nullptr);
         } else {
-          x = lse[row0 + g] / kLn2;
+          const float2 whole = work.stats[row0 + g];
+          M = whole.x;
+          sum = whole.y;
         }
-        head_lse[warp][g] = x == -INFINITY ? INFINITY : x;
+        stat[warp][g] = head_stat(M, sum);
       }
       __syncwarp();
       add_weights<T, D>(cache, cache.table + int64_t(b) * cache.max_pages, h, G, t_lo, t_hi,
-                        work.scores + int64_t(first) * L::kUnit * G, head_lse[warp], lane,
-                        32);
+                        work.scores + int64_t(first) * L::kUnit * G, stat[warp], scale, lane, 32);
       __syncwarp();
       u = u_end;
     }
@@ -947,10 +973,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     }
     if (warp == 0) {
       float M, sum;
-      join_stats<32>(pieces, G, g, lane, M, sum, scale);
+      join_stats<32>(pieces, G, g, lane, scale, M, sum, counts);
       if (lane == 0) {
         total = sum;
-        lse[row] = final_lse2(M, sum) * kLn2;
+        lse[row] = final_lse(M, sum, scale);
       }
     }
     __syncthreads();
@@ -958,11 +984,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
       const int i = r + k * kRows;
-      if (i < pieces.n) out = fmaf(scale[i], held[k], out);
+      if (i < pieces.n) out = fmaf(counts[i], held[k], out);
     }
 #pragma unroll 8
     for (int i = r + kHeld * kRows; i < pieces.n; i += kRows)
-      out = fmaf(scale[i], pieces[i][2 * G + g * D + e], out);
+      out = fmaf(counts[i], pieces[i][2 * G + g * D + e], out);
     red[r][e] = out;
     __syncthreads();
     if (r == 0) {

@@ -108,3 +108,55 @@ def test_outputs_are_not_cut_off(d, dtype):
     rms = math.sqrt((o ** 2).mean())
     assert rms <= 2.0 ** -23, rms * 2.0 ** 24
     assert np.abs(o).max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("max_pages", [None, 4096])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+def test_lse_is_rounded_once(dtype, d, max_pages):
+    """One slot a sequence, its product with the query exact: LSE is the
+    product times the scale and half a step of float32 off at most."""
+    c = Case(dtype, lens=(1,) * 256, Hkv=1, G=1, d=d, max_pages=max_pages)
+    keys = bf16(np.linspace(-700, 900, 256))
+    c.k.zero_()
+    c.k[c.table[:, 0].long(), 0, 0, 0] = c.k.new_tensor(keys)
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.cfg.scale = float(np.float32(d ** -0.5))
+    c.decode()
+    want = keys * c.cfg.scale
+    err = np.abs(c.lse[:, 0].double().cpu().numpy() - want)
+    assert (err <= 2.0 ** -24 * np.abs(want)).all(), (err / np.abs(want)).max() * 2.0 ** 24
+
+
+@pytest.mark.parametrize("lens,max_pages", [
+    ((64, 30, 5), None),            # one launch
+    ((64, 30, 5), 4096),            # two launches, whole heads
+    ((64,) * 300 + (0, 1), 512),    # most heads whole, some split between two blocks
+    ((700,), 4096),                 # one head, split
+])
+@pytest.mark.parametrize("offset", [300.0, -300.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_of_a_head_add_up_to_its_query_heads(dtype, offset, lens, max_pages):
+    """The softmax weights of a head add up to 1 a query head, however large
+    LSE is and wherever the blocks' runs are cut.  Each weight is good to
+    2^-21 next to its sum (ex2 2^-22 each), the sum to 2^-20 (up to 16
+    additions one after the other), the additions to the records and 1 / sum to
+    2^-21: bound 2^-19."""
+    import torch
+    c = Case(dtype, lens=lens, Hkv=2, G=2, max_pages=max_pages)
+    # every score is the offset and a little
+    c.k *= 0.125
+    c.k[..., 0] = 1.0
+    c.q.mul_(0.5)
+    c.q[..., 0] = offset * 128 ** 0.5
+    c.weight.zero_()
+    c.decode(True)
+    lse = c.lse[torch.tensor([n > 0 for n in lens], device="cuda")]
+    assert 200 < float(lse.abs().min()) and float(lse.abs().max()) < 400
+    w, table = c.weight.double().cpu().numpy(), c.table.cpu().numpy()
+    for b, n in enumerate(lens):
+        pg, row, _ = ref.places(table[b], n, c.ps, c.k.shape[0])
+        for h in range(2):
+            total = w[pg, h, row].sum()
+            assert abs(total - 2 * (n > 0)) <= 2 * 2.0 ** -19, (b, h, (total - 2) * 2.0 ** 20)
+    assert status() == 0
