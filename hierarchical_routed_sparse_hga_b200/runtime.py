@@ -14,6 +14,8 @@ just moving q_begin forward: later segments read the same tokens, detached
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib
@@ -340,7 +342,8 @@ class HgaPagedLayer:
 
         advance(n_new); append(...); decode(...)      [; evict(keep, ...)]
 
-    with one `advance` per step however many layers share the counts.
+    with one `advance` per step however many layers share the counts, all on
+    the current stream or all with the same `stream`.
     """
 
     def __init__(self, cfg: Config, n_pages: int, page_size: int, max_pages: int, device="cuda",
@@ -369,10 +372,19 @@ class HgaPagedLayer:
             ws = max(ws, _lib.hga_paged_evict_workspace_size(cfg, self.cache))
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
 
-    def advance(self, n_new):
+    def _on(self, stream):
+        """Context in which torch's operations run on `stream` (as the calls take it)."""
+        if stream is None:
+            return contextlib.nullcontext()  # the current one
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.cache.device)
+        return torch.cuda.stream(stream)
+
+    def advance(self, n_new, stream=None):
         """n_new (an int, or an int32 tensor [batch]) tokens join each sequence."""
-        self.n_slots.add_(n_new)
-        self.pos.add_(n_new)
+        with self._on(stream):
+            self.n_slots.add_(n_new)
+            self.pos.add_(n_new)
 
     @staticmethod
     def _rows(x, heads, d, name):
@@ -423,9 +435,5 @@ class HgaPagedLayer:
         _lib.hga_paged_evict(self.cfg, self.cache, self.n_slots, self.pos, keep, sinks, recent,
                              self.workspace, stream=stream)
         if clamp:
-            if stream is None:
-                stream = torch.cuda.current_stream(self.cache.device)
-            elif isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.cache.device)
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 self.n_slots.clamp_(max=keep)
