@@ -521,8 +521,9 @@ def _paged_cfg(cache: PagedCache, cfg: Config):
     if cache.shape is not None and cache.shape != (cfg.batch, cfg.n_kv_heads, cfg.head_dim,
                                                    cfg.dtype):
         raise ValueError("the cache was described for another configuration")
-    cache._kept = (dict(cfg.__dict__), ctypes.byref(cfg.c()))
-    return cache._kept[1]
+    # returned from here, not read back: another thread may have stored its own
+    kept = cache._kept = (dict(cfg.__dict__), ctypes.byref(cfg.c()))
+    return kept[1]
 
 
 def _paged_call(name, fn, cache: PagedCache, cfg: Config, stream, *args):
