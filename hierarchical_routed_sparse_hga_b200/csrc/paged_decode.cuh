@@ -40,8 +40,9 @@
 // elements of d) and additions sum those: sums of bf16 products over 64 tiles
 // come out 0.9 * 2^-24 off (root mean square), 4.3 in the unit throughout, for
 // 1 us more.  Float32 operands are split into
-// two tf32 parts and the three largest of the four products are summed: each
-// product is good to 2^-19, where one part alone is good to 2^-9.
+// two tf32 parts (22 bits) and all four products are summed: each is good to
+// 2^-20, where one part alone is good to 2^-9.  An infinite key or value counts as
+// in the formula: the parts of its factor have one sign and none is 0.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -63,6 +64,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 3;
 constexpr int kBlocks = 148 * kBlocksPerSm;  // of the B200's 148 SMs
 constexpr int kMaxG = 8;
+
+// fills the parts of a factor that would be 0, below half a step of float32
+constexpr float kTiny = 0x1p-26f;
 
 // What a product q.k counts.  The reference point of the running softmax moves
 // only when a product exceeds it by more than `slack`, 8 in base 2: the
@@ -159,21 +163,18 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// x = hi + lo in two tf32 numbers of 11 bits.  hi is cut off (K, V: two
-// instructions, and it never overflows) or, nearest, rounded: with a remainder
-// of either sign in one factor, the products of two remainders, which are left
-// out, add up to nothing in the mean.  lo is rounded.  (5 x 4099 slots come out
-// 3.6e-7 off; with every hi cut off 6.2e-7, with lo cut off 7.5e-7; plain float32
-// sums 4.4e-7.)
+// x = hi + lo in two tf32 numbers of 11 bits: hi cut off (it never overflows),
+// lo rounded.  Of an infinity lo is 0: inf - inf is the NaN of all ones, whose
+// rounding carries into the sign.  filled (Q, P: the factors of K and V): lo
+// has the sign of x and is never 0, at least 2^-26 x, so that both parts of
+// it times an infinity are the same infinity.
 struct Split {
   uint32_t hi, lo;
-  __device__ __forceinline__ explicit Split(uint32_t x, bool nearest = false) {
+  __device__ __forceinline__ explicit Split(uint32_t x, bool filled = false) {
     hi = x & 0xffffe000u;
-    if (nearest) {
-      const uint32_t up = (x + 0x1000u) & 0xffffe000u;
-      if ((up & 0x7f800000u) != 0x7f800000u) hi = up;
-    }
-    const float rest = __uint_as_float(x) - __uint_as_float(hi);
+    const float f = __uint_as_float(x);
+    float rest = f - __uint_as_float(hi);
+    if (filled && fabsf(rest) < fabsf(f) * kTiny) rest = f * kTiny;
     lo = (__float_as_uint(rest) + 0x1000u) & 0xffffe000u;
   }
 };
@@ -246,15 +247,13 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q,
       for (int sl = 0; sl < L::kSlabs; ++sl) {
         const uint4 k = kr[sl][0][j];
         const Split kx(k.x), ky(k.y), kz(k.z), kw(k.w);
-        float c[4] = {};
-        mma_tf32(c, a_lo.x, 0u, a_lo.y, 0u, kx.hi, ky.hi);
-        mma_tf32(c, a.x, 0u, a.y, 0u, kx.lo, ky.lo);
-        mma_tf32(c, a_lo.z, 0u, a_lo.w, 0u, kz.hi, kw.hi);
-        mma_tf32(c, a.z, 0u, a.w, 0u, kz.lo, kw.lo);
-        mma_tf32(c, a.x, 0u, a.y, 0u, kx.hi, ky.hi);
-        mma_tf32(c, a.z, 0u, a.w, 0u, kz.hi, kw.hi);
-        s[sl][0][0] += c[0];
-        s[sl][0][1] += c[1];
+        float c[4] = {};  // Q's high parts, and its low ones in the 8 rows below
+        mma_tf32(c, a.x, a_lo.x, a.y, a_lo.y, kx.lo, ky.lo);
+        mma_tf32(c, a.z, a_lo.z, a.w, a_lo.w, kz.lo, kw.lo);
+        mma_tf32(c, a.x, a_lo.x, a.y, a_lo.y, kx.hi, ky.hi);
+        mma_tf32(c, a.z, a_lo.z, a.w, a_lo.w, kz.hi, kw.hi);
+        s[sl][0][0] += c[0] + c[2];
+        s[sl][0][1] += c[1] + c[3];
       }
     }
   }
@@ -300,13 +299,21 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
         acc.l += p[nt][i];
       }
     if constexpr (L::kBf16) {
-      // p = hi + mid + lo in three bf16 numbers of 8 bits, each cut off: exact
+      // p = hi + mid + lo in three bf16 numbers of 8 bits, each cut off: exact,
+      // but for parts of 0 (times an infinite value: NaN), which are filled
       uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        float r[2];
+        const float tiny[2] = {p[nt][0] * kTiny, p[nt][1] * kTiny};
+        float r[2] = {};
+        auto fill = [&] {
+          r[0] = fmaxf(r[0], tiny[0]);
+          r[1] = fmaxf(r[1], tiny[1]);
+        };
         hi[nt] = bf16_parts(p[nt], r);
+        fill();
         mid[nt] = bf16_parts(r, r);
+        fill();
         lo[nt] = bf16_parts(r, r);
       }
 #pragma unroll
@@ -338,6 +345,7 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
           const Split a0(w ? u0.z : u0.x), a1(w ? u0.w : u0.y);
           const Split a2(w ? u1.z : u1.x), a3(w ? u1.w : u1.y);
           float c[4] = {};  // added below: see score_tile
+          mma_tf32(c, a0.lo, a1.lo, a2.lo, a3.lo, p0.lo, p1.lo);
           mma_tf32(c, a0.lo, a1.lo, a2.lo, a3.lo, p0.hi, p1.hi);
           mma_tf32(c, a0.hi, a1.hi, a2.hi, a3.hi, p0.lo, p1.lo);
           mma_tf32(c, a0.hi, a1.hi, a2.hi, a3.hi, p0.hi, p1.hi);

@@ -558,9 +558,15 @@ HGA_API size_t hga_paged_decode_workspace_size(const hga_config_t* cfg, const hg
  *   weight[slot] += sum_g exp(s_gj - LSE_g).
  * n_slots[b] = 0: O = 0, LSE = -inf.  Slots on a page outside [0, n_pages)
  * are left out of the softmax.  Rows of the last page behind n_slots[b] are
- * never used, whatever they hold; keys and values of slots in use must be
- * finite (others make their head's results NaN or undefined numbers).  Deterministic (with accumulate = 1 as long
- * as no two sequences share a page).  workspace: at least
+ * never used, whatever they hold.  Infinite and NaN keys and values of slots
+ * in use count as in the formula: a score of -inf has no weight, one of +inf
+ * or NaN makes its query head's results NaN, an infinite value makes its
+ * element infinite (NaN with one of the other sign, or where its weight is 0;
+ * weights below 2^-90 may count as 0 there).  Scores, statistics and sums are
+ * float32, weights enter their product with all of their bits where the dtype
+ * is bf16; where it is float32 every factor enters with 22 bits or more, and a
+ * product is off by 2^-20 of it at most.  Deterministic (with accumulate = 1
+ * as long as no two sequences share a page).  workspace: at least
  * hga_paged_decode_workspace_size() bytes of device memory, 16-byte aligned,
  * whose contents do not matter; not used by two calls at once.  The counts
  * are read on the device, so a captured call follows them.  One launch where
