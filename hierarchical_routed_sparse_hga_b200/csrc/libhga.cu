@@ -1244,7 +1244,7 @@ extern "C" hga_status_t hga_paged_append(const hga_config_t* cfg, const hga_page
                         static_cast<const void*>(n_slots), static_cast<const void*>(pos),
                         static_cast<const void*>(q_out)})
     if (!aligned16(p)) return HGA_ERR_INVALID_ARG;
-  if (s_new < 0 || !(rope_base >= 0.f)) return HGA_ERR_INVALID_ARG;
+  if (s_new < 0 || !(rope_base >= 0.f) || std::isinf(rope_base)) return HGA_ERR_INVALID_ARG;
   const int64_t elt = cfg->dtype == HGA_BF16 ? 2 : 4;
   const int64_t max_stride = int64_t(1) << 32;
   if (kv_row_stride < int64_t(cfg->n_kv_heads) * cfg->head_dim || kv_row_stride * elt % 16 != 0 ||

@@ -526,7 +526,7 @@ typedef struct {
  * NULL: all of them; 0 <= n_new[b] <= n_slots[b]); row i goes to slot
  * n_slots[b] - n_new[b] + i and has position pos[b] - n_new[b] + 1 + i, which
  * must lie in [0, 2^31).  Q and K are rotated as in hga_prepare_segment
- * (rope_base 0 or 1: not rotated), V is not.  q_out [batch, n_q_heads, s_new,
+ * (rope_base from 0 to 1: not rotated; it must be finite), V is not.  q_out [batch, n_q_heads, s_new,
  * head_dim] receives Q (not in place); q_proj and q_out may both be NULL (K
  * and V only).  Where the records are kept, a new slot's weight becomes 0 and
  * its slot_pos its position.  Rows i >= n_new[b] of q_out are left as they

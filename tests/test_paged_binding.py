@@ -1,5 +1,7 @@
 """The paged cache's binding on the CPU: what a call gets is what its caller gave."""
 
+import pytest
+
 import hierarchical_routed_sparse_hga_b200 as hga
 from hierarchical_routed_sparse_hga_b200 import _lib
 
@@ -35,3 +37,13 @@ def test_a_kept_configuration_follows_its_changes():
     assert _lib._paged_cfg(cache, cfg) is cache._kept[1]
     cfg.scale = 0.125
     assert _lib._paged_cfg(cache, cfg)._obj.scale == 0.125
+
+
+def test_append_refuses_an_infinite_rope_base():
+    """Its first pair would turn by the position itself, the others not at all."""
+    cfg = hga.Config(2, 32, 8, 128, 1, 1)
+    cache = hga.PagedCache.raw(FAKE, FAKE, FAKE, 100, 8 * 64 * 128, 64, 10)
+    with pytest.raises(hga.HgaError) as e:
+        hga.hga_paged_append(cfg, cache, FAKE, FAKE, FAKE, 32 * 128, 8 * 128, 1, None, FAKE, FAKE,
+                             float("inf"), FAKE << 8, 0)
+    assert e.value.status == hga.HGA_ERR_INVALID_ARG
