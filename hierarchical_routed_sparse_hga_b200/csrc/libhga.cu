@@ -1420,12 +1420,16 @@ extern "C" hga_status_t hga_paged_evict(const hga_config_t* cfg, const hga_pages
   const hga_status_t e = select(pev::paged_evict_kernel<char, 0>);
   if (e != HGA_OK) return e;
   return dispatch(cfg, [&]<typename T, int D>() -> hga_status_t {
-    // One wave: four blocks of moves fit on an SM (8 x 32768 slots cut to 8192:
-    // 108 us, with eight 110, with twelve 113; 53 x 2479, one KV head: 16.3, 18.7).
-    // Several long sequences may differ much in length, and then more and
-    // smaller blocks even out who has what to move (31 x 4 heads, up to 20701
-    // slots: 62 us with eight an SM, 77 with four).
-    const int per_sm = cfg->batch >= 4 && slots >= 8192 ? 8 : 4;
+    // One wave: four blocks of moves fit on an SM.  Sequences of a batch may
+    // differ much in length (the host does not see it), and then more and
+    // smaller blocks even out who has what to move, for some 2 us of their own:
+    // eight where there are enough sequences and slots for it.  Four against
+    // eight, us, ragged and even batches of (sequences x heads, slots):
+    //   31 x 4, 20701: 76, 62 and 110, 109    8 x 8, 32768: 81, 75 and 108, 110
+    //   4 x 8, 32768: 45, 38 and 62, 64       64 x 8, 4096: 90, 86 and 122, 123
+    //   16 x 8, 6000: 41, 40 and 53, 54       39 x 4, 3059: 28, 28 and 35, 36
+    //   5 x 4, 12000: 23, 24 and 28, 30       3 x 8, 32768: 37, 39 and 42, 45
+    const int per_sm = cfg->batch >= 4 && heads * slots >= (1 << 19) ? 8 : 4;
     const int64_t x = std::max<int64_t>(1, per_sm * int64_t(sm_count()) / heads);
     dim3 grid(unsigned(std::min<int64_t>(x, (slots + 63) / 64)), cfg->n_kv_heads, cfg->batch);
     return traced_launch(HGA_K_PAGED_MOVE, s, [&] {
