@@ -1313,8 +1313,10 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
     while (nc < pdec::kMaxC && nc < units && 2 * nc * heads <= pdec::kBlocks) nc *= 2;
     if (heads <= pdec::kBlocks && units <= int64_t(nc) * pdec::kFewUnits<T>) {
       const size_t smem = pdec::few_bytes<T, D>(G, accumulate != 0);
-      hga_status_t e = ensure_smem(
-          reinterpret_cast<const void*>(&pdec::paged_decode_few_kernel<T, D>), smem);
+      const auto kernel = nc * heads <= 148 * pdec::kFewPerSm
+                              ? &pdec::paged_decode_few_kernel<T, D, pdec::kFewPerSm>
+                              : &pdec::paged_decode_few_kernel<T, D, pdec::kBlocksPerSm>;
+      hga_status_t e = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
       if (e != HGA_OK) return e;
       return traced_launch(HGA_K_PAGED_DECODE, s, [&] {
         cudaLaunchConfig_t lc = {};
@@ -1331,9 +1333,8 @@ extern "C" hga_status_t hga_paged_decode(const hga_config_t* cfg, const hga_page
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         lc.attrs = attr;
         lc.numAttrs = 2;
-        return cudaLaunchKernelEx(&lc, pdec::paged_decode_few_kernel<T, D>, view,
-                                  static_cast<const T*>(q), n_slots, G, int(accumulate),
-                                  scale, static_cast<T*>(o), lse);
+        return cudaLaunchKernelEx(&lc, kernel, view, static_cast<const T*>(q), n_slots, G,
+                                  int(accumulate), scale, static_cast<T*>(o), lse);
       });
     }
     const pdec::Work work = paged_work(cfg, cache, accumulate != 0, workspace).work;

@@ -34,15 +34,15 @@
 // results are deterministic.
 //
 // Precision.  Statistics and sums are float32.  P enters its product as three
-// bf16 parts, which hold all of its 24 bits (two parts hold 16: 1 us of 163
-// less at 8 x 32768 slots, and errors of 2^-17).  The matrix unit cuts its sums
-// off instead of rounding them, so it forms short ones only (16 slots, 16 or 32
-// elements of d) and additions sum those: sums of bf16 products over 64 tiles
-// come out 0.9 * 2^-24 off (root mean square), 4.3 in the unit throughout, for
-// 1 us more.  Float32 operands are split into
-// two tf32 parts (22 bits) and all four products are summed: each is good to
-// 2^-20, where one part alone is good to 2^-9.  An infinite key or value counts as
-// in the formula: the parts of its factor have one sign and none is 0.
+// bf16 parts, which hold all of its 24 bits (two hold 16, and the remainder
+// shows in bf16 outputs).  The matrix unit cuts its sums off instead of rounding
+// them, so it forms short ones only (16 slots, 16 or 32 elements of d) and
+// additions sum those: sums of bf16 products over 64 tiles come out 0.9 * 2^-24 off
+// (root mean square), 4.3 in the unit throughout, which would take 1.5 % less
+// time.  Float32 operands are split into two tf32 parts (22 bits) and all four
+// products are summed: each is good to 2^-20, where one part alone is good to
+// 2^-9.  An infinite key or value counts as in the formula: the parts of its factor
+// have one sign and none is 0.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -57,7 +57,7 @@ namespace pdec {
 
 // 12 warps on an SM: with 168 registers a thread a tile of K and of V and the
 // output stay in registers; 16 warps of 128 spill, and read 8 x 32768 slots
-// (bf16, 8 heads, d = 128; 1.07 GB) in 187 us instead of 160 (6.7 TB/s).
+// (bf16, 8 heads, d = 128; 1.07 GB) in 202 us instead of 163 (6.6 TB/s).
 // Small blocks, so that one merges its warps while another reads.
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
@@ -121,7 +121,7 @@ struct Work {
 // each head counts that many more where the runs are cut: position p of a
 // head that begins at unit u0 is its unit p - u0 - kHeadUnits.  Without it a
 // block that gets many short sequences is the last to end: 64 sequences of 0
-// to 8190 slots take 183 us instead of 166.
+// to 8190 slots take 186 us instead of 168.
 constexpr int kHeadUnits = 2;
 
 // The runs of the blocks in use: q units each, the first r one more.
@@ -153,6 +153,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4],
+                                         const uint32_t (&b)[2]) {
+  mma_bf16(c, a[0], a[1], a[2], a[3], b[0], b[1]);
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -238,7 +243,7 @@ __device__ __forceinline__ void score_tile(const KR& kr, const uint4* q,
         }
     }
   } else {
-    // (4 x 16384 slots come out 5.3e-7 off, plain float32 sums 1.5e-6, sums in
+    // (4 x 16384 slots come out 4.7e-7 off, plain float32 sums 1.2e-6, sums in
     // the unit alone 2.8e-6)
 #pragma unroll
     for (int j = 0; j < L::kKc; ++j) {
@@ -316,25 +321,33 @@ __device__ __forceinline__ void add_tile(Acc<T, D>& acc, const VR& vr,
         fill();
         lo[nt] = bf16_parts(r, r);
       }
+      // four products side by side: each is a chain of three instructions
 #pragma unroll
-      for (int x = 0; x < L::kVc; ++x)
+      for (int x = 0; x < L::kVc; ++x) {
+        uint32_t a[4][4];
+        float c[4][4] = {};  // added below: see score_tile
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           auto word = [&](int r) {
             const uint4& u = vr[sl][r][x];
             return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w;
           };
-          const uint32_t a0 = __byte_perm(word(0), word(1), 0x5410);
-          const uint32_t a1 = __byte_perm(word(0), word(1), 0x7632);
-          const uint32_t a2 = __byte_perm(word(2), word(3), 0x5410);
-          const uint32_t a3 = __byte_perm(word(2), word(3), 0x7632);
-          float c[4] = {};  // added below: see score_tile
-          mma_bf16(c, a0, a1, a2, a3, lo[0], lo[1]);
-          mma_bf16(c, a0, a1, a2, a3, mid[0], mid[1]);
-          mma_bf16(c, a0, a1, a2, a3, hi[0], hi[1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc.o[x * 4 + w][i] += c[i];
+          a[w][0] = __byte_perm(word(0), word(1), 0x5410);
+          a[w][1] = __byte_perm(word(0), word(1), 0x7632);
+          a[w][2] = __byte_perm(word(2), word(3), 0x5410);
+          a[w][3] = __byte_perm(word(2), word(3), 0x7632);
         }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mma_bf16(c[w], a[w], lo);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mma_bf16(c[w], a[w], mid);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mma_bf16(c[w], a[w], hi);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc.o[x * 4 + w][i] += c[w][i];
+      }
     } else {
       const Split p0(__float_as_uint(p[0][0]), true), p1(__float_as_uint(p[0][1]), true);
 #pragma unroll
@@ -742,13 +755,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // Short caches in one launch: a cluster of nc blocks per (sequence, KV head),
 // each with at most kFewUnits units of its slots; partial results, and the
 // scores for the weights, stay in shared memory and are joined through it.
-// Bound by latency: 1 x 300 slots 5.7 us (with the two kernels above and below
-// 8.6), 1 x 2048 8.2 (10.8), 1 x 4096 12.3 (13.5), 8 x 1024 10.7 (14.5).
+// Bound by latency: 1 x 300 slots 5.9 us (with the two kernels above and below
+// 8.9), 1 x 2048 8.6 (11.0), 1 x 4096 12.7 (13.8), 8 x 1024 11.1 (14.7).
 // ---------------------------------------------------------------------------
 constexpr int kMaxC = 8;
+// Blocks an SM is built for: with few warps on it a warp's own chain through a tile
+// counts, and the registers of two blocks an SM shorten it (1 x 4096 slots 12.7
+// us, 13.7 with those of three); more blocks than 2 x 148 are to run at once all
+// the same (25 x 4 heads of 1000 slots, 400 blocks: 13.8 us, in two launches 18.0).
+constexpr int kFewPerSm = 2;
 // a float32 tile takes more instructions: 2 x 2048 slots, 8 units a block, are
-// faster in two launches (17.5 us) than in one (20.5); bf16 the other way
-// round, and from 12 units on two are faster there too (1 x 6144: 15.0, 17.1)
+// faster in two launches (18.0 us) than in one (19.6); bf16 the other way
+// round, and from 12 units on two are faster there too (1 x 6144: 15.1, 17.6)
 template <typename T>
 constexpr int kFewUnits = sizeof(T) == 2 ? 8 : 4;
 
@@ -767,10 +785,10 @@ __host__ __device__ constexpr size_t few_bytes(int G, bool accumulate) {
          (accumulate ? size_t(kFewUnits<T>) * Tile<T, D>::kUnit * G * 4 : 0);
 }
 
-// grid (nc, n_kv_heads, batch) in clusters of (nc, 1, 1); the table holds at
-// most nc * kFewUnits units
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+// grid (nc, n_kv_heads, batch) in clusters of (nc, 1, 1), kPerSm blocks on an SM;
+// the table holds at most nc * kFewUnits units
+template <typename T, int D, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm)
     paged_decode_few_kernel(PagedView cache, const T* __restrict__ q,
                             const int32_t* __restrict__ n_slots, int G, int accumulate,
                             Scale scale, T* __restrict__ o, float* __restrict__ lse) {

@@ -591,6 +591,8 @@ HGA_API size_t hga_paged_evict_workspace_size(const hga_config_t* cfg, const hga
  * kept slots at or behind `keep`, in ascending order, are copied with their
  * records into the dropped slots before it, in ascending order.  Afterwards
  * the kept tokens fill slots [0, keep); slots behind are left as they were.
+ * A slot's weight is 0 until a decode with accumulate = 1 has run: straight
+ * after a prompt all weights tie, and the lowest slots are kept.
  * The caller then sets n_slots[b] to min(n_slots[b], keep) (the call does not,
  * since the layers of a model share the counts) and may free the pages behind.
  * Needs cache->weight and cache->slot_pos.  keep >= 1, sinks and recent >= 0,

@@ -25,6 +25,22 @@ def test_evict_with_wide_tables(kw, keep):
     assert status() == 0
 
 
+@pytest.mark.parametrize("kw", [
+    # one launch: two blocks an SM, and just more than that; clusters of four
+    dict(lens=(33, 1, 17, 0) * 9 + (40,), Hkv=8, G=1, d=64), dict(lens=(33, 1, 17, 0) * 10, Hkv=8, G=1, d=64),
+    dict(lens=(300, 2, 0, 190, 77) * 5, Hkv=4, G=2, d=64, ps=32), dict(lens=(90,) * 37, Hkv=12, G=2, ps=32),
+    # as many heads as the GPU holds blocks, and one more
+    dict(lens=(20, 5) * 37, Hkv=6, G=1, d=64), dict(lens=(20, 5, 9, 1, 16) * 89, Hkv=1, G=3, d=64),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_of_many_short_caches(kw, dtype):
+    c = Case(dtype, **kw)
+    before = c.host()[2]
+    c.decode(True)
+    c.check_decode(before)
+    assert status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_weights_through_the_steps_of_a_generation(dtype):
     """Captured steps of append + decode over a cache that is cut now and then:
