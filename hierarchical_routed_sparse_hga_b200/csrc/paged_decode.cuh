@@ -732,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                    work.scores ? work.scores + int64_t(sh.first) * L::kUnit * G : nullptr, sh.q, acc);
     }
     const int64_t row0 = (int64_t(sh.seq) * n_kv + sh.head) * G;
-    merge_warps(acc, sh.wo, sh.wm, sh.wl, G, scale, [&](int g, int e, float M, float sum, float out) {
+    merge_warps(acc, sh.wo, sh.wm, sh.wl, G, scale,
+                [&](int g, int e, float M, float sum, float out) {
       if (sh.part < 0) {
         o[(row0 + g) * D + e] = final_out<T>(out, sum);
         if (e == 0) {
